@@ -297,6 +297,91 @@ lkv_status lkv_latent_cache_append_fp8(const void* new_rows, int64_t new_row_str
                                        lkv_stream_t stream);
 
 /*
+ * Paged 4-bit latent cache: rotary positions, the append and decode attention.
+ *
+ * The pages do not describe this cache (they say only that serving is bound by KV bytes and runs below
+ * bf16: Grouped Latent Attention article, section on the GLA-vs-MLA decoding test); the formats are
+ * the library's own.
+ *
+ * Rotary positions.  Pair i of rot / 2, (a, b), of a token at position p becomes
+ *   a' = gain (a cos(p freqs[i]) - b sin(p freqs[i])),  b' = gain (a sin(p freqs[i]) + b cos(p freqs[i]))
+ * (inverse != 0: with the angle negated, the transpose of that map, so its gradient).  Pair i is
+ * columns first + i and first + i + rot / 2 of each head (the half layout), or first + 2 i and
+ * first + 2 i + 1 (interleaved != 0).  The other columns are copied.
+ *   x          [n_tok, heads, d] bf16 or fp32 (dtype), unit inner stride, strides in elements
+ *   positions  [n_tok] int32;  freqs [rot / 2] fp64, radians a position (long-context scalings change
+ *              freqs and gain).  Angles are taken in fp64, products in fp32.
+ *   out        as x; the same array and strides (in place) or one that does not overlap x
+ * rot even, at most 1024 (LKV_ERR_UNSUPPORTED); gain finite and > 0.  n_tok = 0 launches nothing.
+ */
+lkv_status lkv_rope_rotate(const void* x, int64_t x_token_stride, int64_t x_head_stride,
+                           const int32_t* positions, const double* freqs, int64_t n_tok, int heads, int d,
+                           int first, int rot, int interleaved, int inverse, float gain, int dtype,
+                           void* out, int64_t out_token_stride, int64_t out_head_stride,
+                           lkv_stream_t stream);
+
+/*
+ * A 4-bit cache row (one token) of r latent columns and d_rope RoPE columns, of
+ * lkv_int4_cache_row_bytes(r, d_rope) bytes:
+ *   [0, r / 2)   4-bit codes u = code + 8, code in [-7, 7].  Eight columns share a little-endian 32-bit
+ *                word: column 2i of the eight in bits 4i .. 4i+3, column 2i+1 in bits 16+4i .. 19+4i
+ *   then         r / 32 bf16 scales, one for every 32 columns; zeros up to a multiple of 16 bytes
+ *   then         d_rope bf16 values: the (rotated) RoPE key
+ * The latent held is code * scale, exact in bf16: a scale is the smallest number of 4 significant bits
+ * with 7 scale >= amax (amax the largest magnitude of the 32 columns); it is 0, with every code 0,
+ * where amax < 2^-100.  code = x / scale rounded to the nearest integer, ties to even.
+ * lkv_int4_cache_row_bytes returns 0 unless r is a multiple of 32 in [32, 1024] and d_rope a multiple of
+ * 8 in [0, 1024] (host-only, no CUDA call).
+ */
+size_t lkv_int4_cache_row_bytes(int r, int d_rope);
+
+/*
+ * The pool: n_pages pages of page_size rows; row s of page p starts at byte p * page_stride_bytes +
+ * s * row_stride_bytes (both multiples of 16, pool 16-byte aligned).  Token t of request b is row
+ * t % page_size of page block_table[b * table_stride + t / page_size].  seq_lens [batch] int32 counts
+ * the tokens of each request, the new ones among them; 0 (or less) is an idle slot.  Any page size;
+ * entries of the table that no token needs are never read as pages and may hold anything.
+ *
+ * Append: rotate, quantise and place the new rows.
+ *   new_rows  [n_new, r + d_rope] bf16 (latent, then the RoPE key), row stride a multiple of 8 elements,
+ *             16-byte aligned; values finite and below 2^100 in magnitude
+ *   cu_new    [batch + 1] int32, device: rows cu_new[b] .. cu_new[b+1] - 1 are the newest of request b
+ *             (rows from cu_new[batch] on are ignored); NULL: n_new / batch rows for every request
+ *   freqs     [d_rope / 2] fp64 with `interleaved` and `gain` as above: the key is rotated to its
+ *             position, which is the token's index; NULL: stored as it comes
+ *   rows_out  NULL, or [n_new, r + d_rope] bf16: the values the cache now holds (may be new_rows itself)
+ * A row whose index would be negative (more new rows than seq_lens counts) is skipped; one without a
+ * page (past the table, or a page outside [0, n_pages)) is skipped and recorded as LKV_SITE_BAD_ROW.
+ * Two rows with the same place in one call race.
+ */
+lkv_status lkv_paged_append_int4(const void* new_rows, int64_t new_row_stride, int64_t n_new, void* pool,
+                                 int64_t page_stride_bytes, int64_t row_stride_bytes, int64_t n_pages,
+                                 int page_size, const int32_t* block_table, int64_t table_stride,
+                                 int max_pages, const int32_t* seq_lens, const int32_t* cu_new, int batch,
+                                 int r, int d_rope, const double* freqs, int interleaved, float gain,
+                                 void* rows_out, int64_t rows_out_stride, lkv_stream_t stream);
+
+/*
+ * Decode attention over the pool, for the forms whose state is key and value: group j's heads read
+ * columns j * d .. (j+1) * d - 1 of the latent (r = groups * d) and the shared RoPE key.  GTA is d = 128,
+ * GLA d = 256, the MLA absorbed path groups = 1, d = 512 (q with W_UK folded in).
+ *   q [batch, s_q, h_q, d], q_rope [batch, s_q, h_q, d_rope] bf16 contiguous, q_rope rotated
+ *   out [batch, s_q, h_q, d] bf16, lse [batch, s_q, h_q] fp32
+ * Query i sees tokens 0 .. seq_lens[b] - s_q + i; one that sees none (an idle slot, or the older query
+ * of a one-token request) gets out = 0 and lse = -inf.  A token without a page counts as a row of zeros
+ * and is recorded as LKV_SITE_BAD_ROW.  Rows behind a request's last token are not read as values.
+ * Implemented: d 128, 256 or 512, groups * d <= 1024, d_rope = 64, s_q 1 or 2, s_q * h_q / groups <= 256.
+ * workspace_bytes >= lkv_paged_decode_workspace_size(...) (host-only, no CUDA call; 0 on bad input).
+ */
+size_t lkv_paged_decode_workspace_size(int batch, int s_q, int h_q, int groups, int d, int num_sms);
+lkv_status lkv_paged_decode_int4(const void* q, const void* q_rope, const void* pool,
+                                 int64_t page_stride_bytes, int64_t row_stride_bytes, int64_t n_pages,
+                                 int page_size, const int32_t* block_table, int64_t table_stride,
+                                 int max_pages, const int32_t* seq_lens, int batch, int s_q, int h_q,
+                                 int groups, int d, int d_rope, float scale, void* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, lkv_stream_t stream);
+
+/*
  * Merge attention results computed over disjoint key sets (split-KV combine):
  *   lse[r] = ln sum_p exp(lse_parts[p, r]);  out[r, :] = sum_p exp(lse_parts[p, r] - lse[r]) * o_parts[p, r, :]
  *   o_parts [n_parts, rows, d_v] fp32, lse_parts [n_parts, rows] fp32 (a part with lse = -inf

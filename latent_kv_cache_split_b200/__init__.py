@@ -11,11 +11,23 @@ Functions (same names as the C entry points without the ``lkv_`` prefix):
     mla_decode_workspace_size, group_decode_workspace_size,
     absorb_query, unabsorb_output, expand_latent (the projections either side of the path),
     gta_group_decode, fp8_cache_row_bytes, quantize_latent_fp8, latent_cache_append_fp8
-    (and fp8_cache_fields: views of the fields of FP8 cache rows)
+    (and fp8_cache_fields: views of the fields of FP8 cache rows),
+    rope_rotate, int4_cache_row_bytes, paged_append_int4, paged_decode_int4,
+    paged_decode_workspace_size (and rope_frequencies: the frequencies rope_rotate and the append
+    take; int4_cache_fields: views of the fields of 4-bit cache rows)
+
+One decode step over a paged 4-bit cache (MLA absorbed: groups = 1; tokens already counted in seq_lens):
+    freqs, gain = rope_frequencies(64, factor=8.0, context=4096, device="cuda")
+    rope_rotate(q_rope, positions, freqs, gain=gain, out=q_rope)      # positions int32: seq_lens - s_q + i
+    paged_append_int4(new_rows, pool, 512, block_table, seq_lens, freqs=freqs, gain=gain)
+    out, lse = paged_decode_int4(q_abs, q_rope, pool, 1, block_table, seq_lens, scale)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
+import math
 import os
 
 import torch
@@ -76,6 +88,14 @@ _absorb = _sig("lkv_absorb_query", _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, 
 _unabsorb = _sig("lkv_unabsorb_output", _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp)
 _expand = _sig("lkv_expand_latent", _i32, _vp, _i64, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp)
 _oproj = _sig("lkv_output_projection", _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp)
+_rope = _sig("lkv_rope_rotate", _i32, _vp, _i64, _i64, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _f32,
+             _i32, _vp, _i64, _i64, _vp)
+_int4_row_bytes = _sig("lkv_int4_cache_row_bytes", _sz, _i32, _i32)
+_paged_append = _sig("lkv_paged_append_int4", _i32, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _i32, _vp, _i64, _i32,
+                     _vp, _vp, _i32, _i32, _i32, _vp, _i32, _f32, _vp, _i64, _vp)
+_paged_ws = _sig("lkv_paged_decode_workspace_size", _sz, _i32, _i32, _i32, _i32, _i32, _i32)
+_paged_decode = _sig("lkv_paged_decode_int4", _i32, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _i64, _i32, _vp,
+                     _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp, _sz, _vp)
 
 EXPORTED = ["lkv_version", "lkv_status_string", "lkv_plan_ranges", "lkv_mla_decode_workspace_size",
             "lkv_group_decode_workspace_size", "lkv_mla_absorbed_decode", "lkv_gqla_group_decode",
@@ -84,7 +104,8 @@ EXPORTED = ["lkv_version", "lkv_status_string", "lkv_plan_ranges", "lkv_mla_deco
             "lkv_gqla_group_decode_noalloc", "lkv_absorb_query", "lkv_unabsorb_output",
             "lkv_expand_latent", "lkv_gta_group_decode", "lkv_fp8_cache_row_bytes",
             "lkv_quantize_latent_fp8", "lkv_latent_cache_append_fp8", "lkv_output_projection",
-            "lkv_check_stream", "lkv_gta_group_decode_fp8"]
+            "lkv_check_stream", "lkv_gta_group_decode_fp8", "lkv_rope_rotate", "lkv_int4_cache_row_bytes",
+            "lkv_paged_append_int4", "lkv_paged_decode_workspace_size", "lkv_paged_decode_int4"]
 
 
 class LkvError(RuntimeError):
@@ -489,3 +510,202 @@ def output_projection(o, w_o, out_dtype=torch.float32, out=None, stream=None):
     _ck(_oproj(_ptr(o2), _ptr(w_o), _ptr(out), n, k, d_model, _dtype_code(out), _stream(stream)),
         "lkv_output_projection")
     return out
+
+
+# ------------------------------------------------------------------------------------------------
+# Rotary positions and the paged 4-bit cache
+# ------------------------------------------------------------------------------------------------
+
+@functools.lru_cache(maxsize=None)
+def _sms_of(index: int) -> int:
+    return _num_sms(index)
+
+
+def _on_device(where: str, ref: torch.Tensor, **named):
+    """Every tensor given has to be on ref's GPU."""
+    if ref.device.type != "cuda":
+        raise ValueError(f"{where} takes tensors on a GPU")
+    for name, t in named.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{where}: {name} is on {t.device}, expected {ref.device}")
+
+
+def _call(where: str, device, stream, f, *args):
+    """f(*args, stream) with the tensors' device current, on its current stream unless one is given."""
+    if device.index == torch.cuda.current_device():
+        _ck(f(*args, _stream(stream)), where)
+    else:
+        with torch.cuda.device(device):
+            _ck(f(*args, _stream(stream)), where)
+
+
+def _alloc_on(stream):
+    """Allocations for a call on `stream`: from that stream's pool, so that a workspace freed at the call's return is
+    not handed to another stream while the kernels run."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _int32(**named):
+    for name, t in named.items():
+        if t is not None and t.dtype != torch.int32:
+            raise TypeError(f"{name} is {t.dtype}, expected torch.int32")
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, factor: float = 1.0, context: int = 4096,
+                     beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+    """(freqs fp64 [rot / 2] in radians a position, gain) for rope_rotate and paged_append_int4.
+
+    freqs[i] = base^(-2i / rot).  With factor > 1, for a context `factor` times the `context` that was trained
+    on: a pair that turns more than beta_fast times over `context` keeps its frequency, one that turns less than
+    beta_slow times has it divided by factor, with a linear ramp between; gain = 1 + 0.1 ln factor.
+    beta_fast = inf divides every frequency (linear interpolation of the positions)."""
+    if rot <= 0 or rot % 2 or not base > 0 or not factor >= 1 or context <= 0 or not 0 <= beta_slow < beta_fast:
+        raise ValueError("rope_frequencies: rot even and positive, base > 0, factor >= 1, context > 0, "
+                         "0 <= beta_slow < beta_fast")
+    f = float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    gain = 1.0
+    if factor > 1:
+        turns = context * f / (2 * math.pi)
+        keep = (turns - beta_slow) / (beta_fast - beta_slow) if math.isfinite(beta_fast) else torch.zeros_like(f)
+        keep = keep.clamp(0.0, 1.0)
+        f = f * (keep + (1.0 - keep) / factor)
+        gain = 1.0 + 0.1 * math.log(factor)
+    return f.to(device), gain
+
+
+def rope_rotate(x, positions, freqs, first=0, interleaved=False, inverse=False, gain=1.0, out=None, stream=None):
+    """Rotate columns first .. first + 2 len(freqs) - 1 of every head of x [..., heads, d] (bf16 or fp32, unit inner
+    stride) to the tokens' positions (int32, one for each token of x's leading dimensions); the other columns are
+    copied.  Pairs are columns (i, i + rot / 2) of that part, or (2i, 2i + 1) if interleaved.  inverse=True applies
+    the transpose: the gradient of x from the gradient of the result.  out: a new tensor, or x itself (in place), or
+    one that does not overlap x.  Returns out."""
+    _same_dtype(x, out=out)
+    _int32(positions=positions)
+    if freqs.dtype != torch.float64:
+        raise TypeError(f"freqs is {freqs.dtype}, expected torch.float64")
+    _on_device("rope_rotate", x, positions=positions, freqs=freqs, out=out)
+    if x.dim() < 3 or x.stride(-1) != 1:
+        raise ValueError("x must be [..., heads, d] with unit inner stride")
+    if out is None:
+        with _alloc_on(stream):
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape or out.stride(-1) != 1 or (out.data_ptr() == x.data_ptr() and out.stride() != x.stride()):
+        raise ValueError("out must have x's shape and unit inner stride, and x's strides if it is x's memory")
+    heads, d = x.shape[-2:]
+    xs, os_ = (x, out) if x.dim() == 3 else (x.view(-1, heads, d), out.view(-1, heads, d))
+    n = xs.shape[0]
+    if positions.numel() != n:
+        raise ValueError("positions must hold one position for each token")
+    if freqs.dim() != 1 or not freqs.is_contiguous() or not positions.is_contiguous():
+        raise ValueError("freqs must be [rot / 2]; freqs and positions contiguous")
+    if n == 0 and heads > 0 and d > 0:
+        return out
+    _call("lkv_rope_rotate", x.device, stream, _rope, _ptr(xs), xs.stride(0), xs.stride(1), _ptr(positions), _ptr(freqs),
+          n, heads, d, int(first), 2 * freqs.numel(), int(interleaved), int(inverse), float(gain), _dtype_code(x),
+          _ptr(os_), os_.stride(0), os_.stride(1))
+    return out
+
+
+def int4_cache_row_bytes(r: int, d_rope: int) -> int:
+    """Bytes of one 4-bit cache row (codes, bf16 scales, bf16 RoPE key); 0 if unsupported."""
+    return _int4_row_bytes(r, d_rope)
+
+
+def int4_cache_fields(pool, r: int, d_rope: int):
+    """Views of the fields of 4-bit cache rows pool [..., >= row_bytes] uint8: (codes uint8 [..., r / 2],
+    scales bf16 [..., r / 32], k_rope bf16 [..., d_rope])."""
+    rb = int4_cache_row_bytes(r, d_rope)
+    if rb == 0 or pool.dtype != torch.uint8 or pool.shape[-1] < rb or pool.stride(-1) != 1:
+        raise ValueError("pool must be [..., >= row_bytes] uint8 rows")
+    return (pool[..., :r // 2], pool[..., r // 2:r // 2 + r // 16].view(torch.bfloat16),
+            pool[..., rb - 2 * d_rope:rb].view(torch.bfloat16))
+
+
+def _pool_args(where, ref, pool, block_table, seq_lens):
+    """The pool's and table's arguments of the C calls, up to seq_lens and the batch."""
+    if pool.dtype != torch.uint8:
+        raise TypeError(f"{where} takes a uint8 pool")
+    _int32(block_table=block_table, seq_lens=seq_lens)
+    _on_device(where, ref, pool=pool, block_table=block_table, seq_lens=seq_lens)
+    if pool.dim() != 3 or pool.stride(2) != 1:
+        raise ValueError("pool must be [pages, page_size, >= row_bytes] with contiguous rows")
+    B = seq_lens.numel()
+    if (block_table.dim() != 2 or block_table.shape[0] != B or block_table.stride(1) != 1 or seq_lens.dim() != 1
+            or not seq_lens.is_contiguous()):
+        raise ValueError("block_table must be [batch, max_pages] with contiguous rows, seq_lens [batch] contiguous")
+    return (_ptr(pool), pool.stride(0), pool.stride(1), pool.shape[0], pool.shape[1], _ptr(block_table),
+            block_table.stride(0) if B > 1 else block_table.shape[1], block_table.shape[1], _ptr(seq_lens)), B
+
+
+def paged_append_int4(new_rows, pool, r, block_table, seq_lens, cu_new=None, freqs=None, gain=1.0, interleaved=False,
+                      rows_out=None, stream=None):
+    """Append the new rows [n, r + d_rope] bf16 (latent, then RoPE key) to the 4-bit pool [pages, page_size,
+    >= int4_cache_row_bytes(r, d_rope)] uint8, the key rotated to its position on the way (freqs and gain of
+    rope_frequencies; freqs=None: stored as it comes).  seq_lens [batch] int32 counts each request's tokens, the new
+    ones among them; rows cu_new[b] .. cu_new[b + 1] - 1 are the newest of request b (cu_new=None: n / batch each).
+    rows_out: gets the values the cache now holds (bf16, new_rows' shape; may be new_rows).  Returns pool."""
+    _same_dtype(new_rows, rows_out=rows_out)
+    if new_rows.dtype != torch.bfloat16:
+        raise TypeError("paged_append_int4 takes bf16 rows")
+    _int32(cu_new=cu_new)
+    if freqs is not None and freqs.dtype != torch.float64:
+        raise TypeError(f"freqs is {freqs.dtype}, expected torch.float64")
+    args, B = _pool_args("paged_append_int4", new_rows, pool, block_table, seq_lens)
+    _on_device("paged_append_int4", new_rows, cu_new=cu_new, freqs=freqs, rows_out=rows_out)
+    if new_rows.dim() != 2:
+        raise ValueError("new_rows must be [n, r + d_rope]")
+    n, width = new_rows.shape
+    rb = int4_cache_row_bytes(r, width - r)
+    if rb == 0 or pool.shape[2] < rb:
+        raise ValueError("unsupported r / d_rope, or pool rows shorter than int4_cache_row_bytes(r, d_rope)")
+    if cu_new is not None and (cu_new.numel() != B + 1 or not cu_new.is_contiguous()):
+        raise ValueError("cu_new must be [batch + 1], contiguous")
+    if freqs is not None and (freqs.numel() != (width - r) // 2 or not freqs.is_contiguous()):
+        raise ValueError("freqs must be [d_rope / 2], contiguous")
+    if rows_out is not None and rows_out.shape != new_rows.shape:
+        raise ValueError("rows_out must have new_rows' shape")
+    if n == 0:
+        return pool
+    _call("lkv_paged_append_int4", new_rows.device, stream, _paged_append, _ptr(new_rows), _row_stride(new_rows), n,
+          *args, _ptr(cu_new), B, int(r), width - r, _ptr(freqs), int(interleaved), float(gain), _ptr(rows_out),
+          0 if rows_out is None else _row_stride(rows_out))
+    return pool
+
+
+def paged_decode_workspace_size(batch, s_q, h_q, groups, d, num_sms) -> int:
+    return _paged_ws(batch, s_q, h_q, groups, d, num_sms)
+
+
+def paged_decode_int4(q, q_rope, pool, groups, block_table, seq_lens, scale, out=None, lse=None, workspace=None,
+                      stream=None):
+    """Decode attention over a paged 4-bit cache.  q [B,s_q,h_q,d] and q_rope [B,s_q,h_q,64] (rotated) bf16; pool
+    [pages, page_size, >= int4_cache_row_bytes(groups * d, 64)] uint8, whose latent columns j * d .. are key (with the
+    row's RoPE key) and value of group j's heads: d = 128 (GTA), 256 (GLA) or 512 (MLA absorbed, groups = 1).
+    block_table [B, max_pages] and seq_lens [B] int32.  Queries that see no token get out = 0, lse = -inf.
+    Returns (out [B,s_q,h_q,d], lse [B,s_q,h_q] fp32)."""
+    _same_dtype(q, q_rope=q_rope, out=out)
+    if q.dtype != torch.bfloat16:
+        raise TypeError("paged_decode_int4 takes a bf16 query")
+    args, B = _pool_args("paged_decode_int4", q, pool, block_table, seq_lens)
+    _on_device("paged_decode_int4", q, q_rope=q_rope, out=out, lse=lse, workspace=workspace)
+    if q.dim() != 4 or q.shape[0] != B or q_rope.shape[:-1] != q.shape[:-1]:
+        raise ValueError("q must be [batch, s_q, h_q, d] and q_rope [batch, s_q, h_q, d_rope]")
+    _, s_q, h_q, d = q.shape
+    d_r = q_rope.shape[-1]
+    rb = int4_cache_row_bytes(groups * d, d_r)
+    if rb == 0 or pool.shape[2] < rb:
+        raise ValueError("unsupported groups * d / d_rope, or pool rows shorter than int4_cache_row_bytes(groups * d, d_rope)")
+    with _alloc_on(stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = _alloc_ws(_paged_ws(B, s_q, h_q, groups, d, _sms_of(q.device.index)), q.device)
+    if out.shape != q.shape or lse.shape != q.shape[:-1] or lse.dtype != torch.float32:
+        raise ValueError("out must have q's shape, lse [batch, s_q, h_q] fp32")
+    _contig(q, q_rope, out, lse, workspace)
+    _call("lkv_paged_decode_int4", q.device, stream, _paged_decode, _ptr(q), _ptr(q_rope), *args, B, s_q, h_q,
+          int(groups), d, d_r, float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
+          workspace.numel() * workspace.element_size())
+    return out, lse

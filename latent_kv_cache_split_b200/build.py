@@ -2,9 +2,10 @@
 
     python latent_kv_cache_split_b200/build.py [--verbose]
 
-The library is three translation units: csrc/lkv_api.cu (the decode path; it includes the kernel
-headers), csrc/lkv_proj.cu (the projections, on the tensor-core GEMM of csrc/lkv_gemm.cuh) and
-csrc/lkv_fp8.cu (FP8 latent cache rows).  All link the static CUDA runtime, so the .so only needs
+The library is four translation units: csrc/lkv_api.cu (the decode path; it includes the kernel
+headers), csrc/lkv_proj.cu (the projections, on the tensor-core GEMM of csrc/lkv_gemm.cuh),
+csrc/lkv_fp8.cu (FP8 latent cache rows) and csrc/lkv_paged.cu (rotary positions and the paged 4-bit
+cache).  All link the static CUDA runtime, so the .so only needs
 the NVIDIA driver at run time.
 """
 from __future__ import annotations
@@ -18,8 +19,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "liblkv.so")
-SOURCES = ["lkv_api.cu", "lkv_proj.cu", "lkv_fp8.cu"]
-HEADERS = ["lkv_ptx.cuh", "lkv_sched.cuh", "lkv_decode_tc.cuh", "lkv_decode_swap.cuh", "lkv_decode_swap_wide.cuh", "lkv_mla_pair.cuh", "lkv_gemm.cuh", "lkv_aux.cuh", "lkv_tma_host.h"]
+SOURCES = ["lkv_api.cu", "lkv_proj.cu", "lkv_fp8.cu", "lkv_paged.cu"]
+HEADERS = ["lkv_ptx.cuh", "lkv_sched.cuh", "lkv_decode_tc.cuh", "lkv_decode_swap.cuh", "lkv_decode_swap_wide.cuh", "lkv_mla_pair.cuh", "lkv_gemm.cuh", "lkv_aux.cuh", "lkv_tma_host.h", "lkv_rope.cuh", "lkv_int4.cuh", "lkv_paged_decode.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

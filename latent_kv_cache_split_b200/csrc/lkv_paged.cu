@@ -1,0 +1,213 @@
+// Host side of the paged 4-bit cache (include/lkv.h): rotary positions, the append that rotates and
+// quantises, and decode attention over the pool.  Argument checks make no CUDA call.
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/lkv.h"
+#include "lkv_int4.cuh"
+#include "lkv_paged_decode.cuh"
+#include "lkv_rope.cuh"
+
+lkv_status lkv_internal_device_info(int** err, int* num_sms, unsigned long long* wait_ns);  // lkv_api.cu
+
+namespace {
+
+using namespace lkv;
+
+inline bool al(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+inline bool finite_positive(float v) { return std::isfinite(v) && v > 0.f; }
+
+lkv_status launched() {
+  const cudaError_t e = cudaGetLastError();  // a launch error is not sticky; this clears it for the caller
+  return e == cudaSuccess ? LKV_OK : LKV_ERR_CUDA;
+}
+
+size_t row_bytes_of(int r, int d_rope) {
+  if (r <= 0 || r % kInt4Block || r > kInt4MaxLatent || d_rope < 0 || d_rope % 8 || d_rope > 2 * kRopeMaxPairs) return 0;
+  return static_cast<size_t>(int4_rope_at(r)) + 2 * static_cast<size_t>(d_rope);
+}
+
+// Checks of a pool and its table, and the kernels' view of them.
+lkv_status check_pool(Paged* g, const void* pool, int64_t page_stride, int64_t row_stride, int64_t n_pages, int page_size,
+                      const int32_t* table, int64_t table_stride, int max_pages, const int32_t* seq_lens, int batch,
+                      int r, int d_rope) {
+  const size_t rb = row_bytes_of(r, d_rope);
+  if (!pool || !table || !seq_lens || rb == 0 || batch <= 0 || n_pages <= 0 || page_size <= 0 || max_pages <= 0)
+    return LKV_ERR_INVALID_ARG;
+  if (!al(pool, 16) || page_stride % 16 || row_stride % 16 || row_stride < static_cast<int64_t>(rb) ||
+      table_stride < max_pages)
+    return LKV_ERR_INVALID_ARG;
+  // pages do not overlap: whole pages apart, or their rows interleaved with others' (a view of a wider pool)
+  if (n_pages > 1 && page_stride < static_cast<int64_t>(rb)) return LKV_ERR_INVALID_ARG;
+  g->pool = static_cast<uint8_t*>(const_cast<void*>(pool));
+  g->page_stride = page_stride;
+  g->row_stride = row_stride;
+  g->n_pages = n_pages;
+  g->page_size = page_size;
+  g->table = table;
+  g->table_stride = table_stride;
+  g->max_pages = max_pages;
+  g->seq_lens = seq_lens;
+  return LKV_OK;
+}
+
+template <typename T, int V>
+void launch_rope(const RopeParams& p, bool interleaved, unsigned blocks, cudaStream_t s) {
+  if (interleaved)
+    rope_kernel<T, V, true><<<blocks, kRopeThreads, 0, s>>>(p);
+  else
+    rope_kernel<T, V, false><<<blocks, kRopeThreads, 0, s>>>(p);
+}
+
+}  // namespace
+
+extern "C" {
+
+lkv_status lkv_rope_rotate(const void* x, int64_t x_token_stride, int64_t x_head_stride, const int32_t* positions,
+                           const double* freqs, int64_t n_tok, int heads, int d, int first, int rot, int interleaved,
+                           int inverse, float gain, int dtype, void* out, int64_t out_token_stride,
+                           int64_t out_head_stride, lkv_stream_t stream) {
+  if (!x || !positions || !freqs || !out || n_tok < 0 || heads <= 0 || d <= 0) return LKV_ERR_INVALID_ARG;
+  if (first < 0 || rot <= 0 || rot % 2 || rot > d - first || !finite_positive(gain)) return LKV_ERR_INVALID_ARG;
+  if (dtype != LKV_BF16 && dtype != LKV_FP32) return LKV_ERR_INVALID_ARG;
+  if (rot / 2 > kRopeMaxPairs) return LKV_ERR_UNSUPPORTED;
+  const int size = dtype == LKV_BF16 ? 2 : 4, wide = 16 / size;
+  if (!al(x, size) || !al(out, size) || !al(freqs, 8)) return LKV_ERR_INVALID_ARG;
+  if (n_tok == 0) return LKV_OK;
+  RopeParams p;
+  p.x = x;
+  p.out = out;
+  p.x_ts = x_token_stride;
+  p.x_hs = x_head_stride;
+  p.o_ts = out_token_stride;
+  p.o_hs = out_head_stride;
+  p.pos = positions;
+  p.freqs = freqs;
+  p.n_tok = n_tok;
+  p.heads = heads;
+  p.d = d;
+  p.first = first;
+  p.rot = rot;
+  p.inverse = inverse != 0;
+  p.gain = gain;
+  p.copy = x != out;
+  // 16-byte accesses where every row, and every run of columns in it, starts and ends on 16 bytes
+  const bool vec = al(x, 16) && al(out, 16) && x_token_stride % wide == 0 && x_head_stride % wide == 0 &&
+                   out_token_stride % wide == 0 && out_head_stride % wide == 0 && first % wide == 0 && d % wide == 0 &&
+                   (interleaved ? rot : rot / 2) % wide == 0;
+  const int v = vec ? wide : 1;
+  const int items = (interleaved ? rot / (vec ? wide : 2) : rot / 2 / v) + (p.copy ? (d - rot) / v : 0);
+  p.bx = items < kRopeThreads ? items : kRopeThreads;
+  p.by = kRopeThreads / p.bx;
+  const int rows = p.by * kRopeUnroll;
+  const int chunks = (heads + rows - 1) / rows;
+  p.head_block = (heads + chunks - 1) / chunks;
+  p.tok_block = 1;
+  if (chunks == 1) {
+    const int most = kRopeTable / (rot / 2);
+    p.tok_block = rows / heads < most ? rows / heads : most;
+  }
+  const int64_t blocks = (n_tok + p.tok_block - 1) / p.tok_block * ((heads + p.head_block - 1) / p.head_block);
+  if (blocks > INT_MAX) return LKV_ERR_UNSUPPORTED;
+  const unsigned nb = static_cast<unsigned>(blocks);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (dtype == LKV_BF16) {
+    if (vec)
+      launch_rope<__nv_bfloat16, 8>(p, interleaved, nb, s);
+    else
+      launch_rope<__nv_bfloat16, 1>(p, interleaved, nb, s);
+  } else {
+    if (vec)
+      launch_rope<float, 4>(p, interleaved, nb, s);
+    else
+      launch_rope<float, 1>(p, interleaved, nb, s);
+  }
+  return launched();
+}
+
+size_t lkv_int4_cache_row_bytes(int r, int d_rope) { return row_bytes_of(r, d_rope); }
+
+lkv_status lkv_paged_append_int4(const void* new_rows, int64_t new_row_stride, int64_t n_new, void* pool,
+                                 int64_t page_stride_bytes, int64_t row_stride_bytes, int64_t n_pages, int page_size,
+                                 const int32_t* block_table, int64_t table_stride, int max_pages,
+                                 const int32_t* seq_lens, const int32_t* cu_new, int batch, int r, int d_rope,
+                                 const double* freqs, int interleaved, float gain, void* rows_out,
+                                 int64_t rows_out_stride, lkv_stream_t stream) {
+  AppendParams p;
+  lkv_status st = check_pool(&p.pages, pool, page_stride_bytes, row_stride_bytes, n_pages, page_size, block_table,
+                             table_stride, max_pages, seq_lens, batch, r, d_rope);
+  if (st != LKV_OK) return st;
+  if (!new_rows || n_new < 0 || !al(new_rows, 16) || new_row_stride % 8 || new_row_stride < r + d_rope) return LKV_ERR_INVALID_ARG;
+  if (!cu_new && n_new % batch) return LKV_ERR_INVALID_ARG;
+  if (freqs && (!al(freqs, 8) || !finite_positive(gain))) return LKV_ERR_INVALID_ARG;
+  if (rows_out && (!al(rows_out, 16) || rows_out_stride % 8 || rows_out_stride < r + d_rope)) return LKV_ERR_INVALID_ARG;
+  if (n_new >= INT_MAX / 2) return LKV_ERR_UNSUPPORTED;
+  if (n_new == 0) return LKV_OK;
+  int num_sms;
+  unsigned long long wait_ns;
+  if ((st = lkv_internal_device_info(&p.err, &num_sms, &wait_ns)) != LKV_OK) return st;
+  p.rows = static_cast<const __nv_bfloat16*>(new_rows);
+  p.row_stride = new_row_stride;
+  p.n_new = n_new;
+  p.cu_new = cu_new;
+  p.batch = batch;
+  p.per = cu_new ? 0 : static_cast<int>(n_new / batch);
+  p.r = r;
+  p.d_rope = d_rope;
+  p.freqs = freqs;
+  p.interleaved = interleaved != 0;
+  p.gain = gain;
+  p.held = static_cast<__nv_bfloat16*>(rows_out);
+  p.held_stride = rows_out_stride;
+  constexpr int per_block = kAppendThreads / 32;
+  append_int4_kernel<<<static_cast<unsigned>((n_new + per_block - 1) / per_block), kAppendThreads, 0,
+                       reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  return launched();
+}
+
+size_t lkv_paged_decode_workspace_size(int batch, int s_q, int h_q, int groups, int d, int num_sms) {
+  if (batch <= 0 || s_q <= 0 || h_q <= 0 || groups <= 0 || h_q % groups || d <= 0 || num_sms <= 0) return 0;
+  return 256;
+}
+
+lkv_status lkv_paged_decode_int4(const void* q, const void* q_rope, const void* pool, int64_t page_stride_bytes,
+                                 int64_t row_stride_bytes, int64_t n_pages, int page_size, const int32_t* block_table,
+                                 int64_t table_stride, int max_pages, const int32_t* seq_lens, int batch, int s_q,
+                                 int h_q, int groups, int d, int d_rope, float scale, void* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, lkv_stream_t stream) {
+  PagedDecodeParams p;
+  if (!q || !q_rope || !out || !lse || h_q <= 0 || groups <= 0 || d <= 0 || h_q % groups || !finite_positive(scale))
+    return LKV_ERR_INVALID_ARG;
+  if (!al(q, 16) || !al(q_rope, 16) || !al(out, 16) || !al(lse, 4)) return LKV_ERR_INVALID_ARG;
+  if (s_q != 1 && s_q != 2) return LKV_ERR_UNSUPPORTED;
+  if ((d != 128 && d != 256 && d != 512) || d_rope != 64 || s_q * (h_q / groups) > 256) return LKV_ERR_UNSUPPORTED;
+  if (static_cast<long long>(groups) * d > kInt4MaxLatent) return LKV_ERR_UNSUPPORTED;
+  lkv_status st = check_pool(&p.pages, pool, page_stride_bytes, row_stride_bytes, n_pages, page_size, block_table,
+                             table_stride, max_pages, seq_lens, batch, groups * d, d_rope);
+  if (st != LKV_OK) return st;
+  if (static_cast<long long>(batch) * s_q * h_q >= (1LL << 31)) return LKV_ERR_UNSUPPORTED;
+  int num_sms;
+  unsigned long long wait_ns;
+  if ((st = lkv_internal_device_info(&p.err, &num_sms, &wait_ns)) != LKV_OK) return st;
+  if (!workspace || !al(workspace, 16) ||
+      workspace_bytes < lkv_paged_decode_workspace_size(batch, s_q, h_q, groups, d, num_sms))
+    return LKV_ERR_WORKSPACE;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_rope = static_cast<const __nv_bfloat16*>(q_rope);
+  p.B = batch;
+  p.s_q = s_q;
+  p.h_q = h_q;
+  p.G = groups;
+  p.hpg = h_q / groups;
+  p.d = d;
+  p.d_rope = d_rope;
+  p.scale = scale;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  paged_decode_kernel<<<static_cast<unsigned>(batch) * s_q * h_q, kPagedThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  return launched();
+}
+
+}  // extern "C"
