@@ -16,6 +16,8 @@ namespace {
 
 using namespace lkv;
 
+constexpr int kMaxDevices = 64;
+
 inline bool al(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 inline bool finite_positive(float v) { return std::isfinite(v) && v > 0.f; }
 
@@ -59,6 +61,74 @@ void launch_rope(const RopeParams& p, bool interleaved, unsigned blocks, cudaStr
     rope_kernel<T, V, true><<<blocks, kRopeThreads, 0, s>>>(p);
   else
     rope_kernel<T, V, false><<<blocks, kRopeThreads, 0, s>>>(p);
+}
+
+// Rows of a unit (the MMA's N): the smallest of 16, 32, 64 that holds a group's rows, so that small groups
+// spend no softmax on padding; 64 at most (32 where 512 columns of Q and of a tile fill shared memory), and
+// a group of more rows is several units that read the same tiles.
+int paged_rows(int R, int d) { return R <= 16 ? 16 : R <= 32 || d == 512 ? 32 : 64; }
+
+struct PagedPlan {
+  int N, RB, U, P, lockstep;
+  size_t seg, lse, o, total;  // workspace offsets and size
+};
+
+void paged_plan(PagedPlan* w, int s_q, int h_q, int groups, int d, int num_sms) {
+  const int R = s_q * (h_q / groups);
+  w->N = paged_rows(R, d);
+  w->RB = (R + w->N - 1) / w->N;
+  w->U = groups * w->RB;
+  // Units in lockstep share a request's RoPE keys and scales through L2; not where that leaves more than a
+  // tenth of the SMs without a range, nor for so few units that there is little to share.
+  const int sms = num_sms < kPagedMaxRanges ? num_sms : kPagedMaxRanges;
+  const int whole = w->U <= sms ? sms / w->U * w->U : 0;
+  w->lockstep = w->U >= 4 && 10 * whole >= 9 * sms;
+  w->P = w->lockstep ? whole : sms;
+  auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
+  const size_t slots = 2 * static_cast<size_t>(w->P);
+  w->seg = 0;
+  w->lse = up(slots * sizeof(int));
+  w->o = w->lse + up(slots * w->N * sizeof(float));
+  w->total = w->o + up(slots * w->N * d * sizeof(float));
+}
+
+// The decode kernel, then the combine as its programmatic dependent: its launch overlaps the decode, and its
+// blocks wait for the decode's completion before they read the partials.
+template <int D, int N>
+lkv_status launch_decode(const PagedDecodeParams& p, cudaStream_t s) {
+  using Cfg = PagedCfg<D, N>;
+  static bool ready[kMaxDevices];  // the kernel's attribute is set on a device once
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return LKV_ERR_CUDA;
+  if (!ready[dev]) {
+    if (cudaFuncSetAttribute(paged_decode_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(Cfg::kSmem)) != cudaSuccess) {
+      cudaGetLastError();
+      return LKV_ERR_CUDA;
+    }
+    ready[dev] = true;
+  }
+  paged_decode_kernel<D, N><<<p.P, kPagedThreads, Cfg::kSmem, s>>>(p);
+  const lkv_status st = launched();
+  if (st != LKV_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.P, (N + kPagedCombineWarps - 1) / kPagedCombineWarps);
+  cfg.blockDim = dim3(kPagedCombineWarps * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, N>, p);
+  const lkv_status after = launched();
+  return e == cudaSuccess ? after : LKV_ERR_CUDA;
+}
+
+lkv_status launch_decode_for(const PagedDecodeParams& p, int d, int N, cudaStream_t s) {
+  if (d == 128) return N == 16 ? launch_decode<128, 16>(p, s) : N == 32 ? launch_decode<128, 32>(p, s) : launch_decode<128, 64>(p, s);
+  if (d == 256) return N == 16 ? launch_decode<256, 16>(p, s) : N == 32 ? launch_decode<256, 32>(p, s) : launch_decode<256, 64>(p, s);
+  return N == 16 ? launch_decode<512, 16>(p, s) : launch_decode<512, 32>(p, s);
 }
 
 }  // namespace
@@ -168,8 +238,11 @@ lkv_status lkv_paged_append_int4(const void* new_rows, int64_t new_row_stride, i
 }
 
 size_t lkv_paged_decode_workspace_size(int batch, int s_q, int h_q, int groups, int d, int num_sms) {
-  if (batch <= 0 || s_q <= 0 || h_q <= 0 || groups <= 0 || h_q % groups || d <= 0 || num_sms <= 0) return 0;
-  return 256;
+  if (batch <= 0 || s_q <= 0 || h_q <= 0 || groups <= 0 || h_q % groups || num_sms <= 0) return 0;
+  if ((d != 128 && d != 256 && d != 512) || static_cast<long long>(s_q) * (h_q / groups) > 256) return 0;
+  PagedPlan w;
+  paged_plan(&w, s_q, h_q, groups, d, num_sms);
+  return w.total;
 }
 
 lkv_status lkv_paged_decode_int4(const void* q, const void* q_rope, const void* pool, int64_t page_stride_bytes,
@@ -182,18 +255,19 @@ lkv_status lkv_paged_decode_int4(const void* q, const void* q_rope, const void* 
     return LKV_ERR_INVALID_ARG;
   if (!al(q, 16) || !al(q_rope, 16) || !al(out, 16) || !al(lse, 4)) return LKV_ERR_INVALID_ARG;
   if (s_q != 1 && s_q != 2) return LKV_ERR_UNSUPPORTED;
-  if ((d != 128 && d != 256 && d != 512) || d_rope != 64 || s_q * (h_q / groups) > 256) return LKV_ERR_UNSUPPORTED;
+  if ((d != 128 && d != 256 && d != 512) || d_rope != 64 || s_q * static_cast<long long>(h_q / groups) > 256)
+    return LKV_ERR_UNSUPPORTED;
   if (static_cast<long long>(groups) * d > kInt4MaxLatent) return LKV_ERR_UNSUPPORTED;
   lkv_status st = check_pool(&p.pages, pool, page_stride_bytes, row_stride_bytes, n_pages, page_size, block_table,
                              table_stride, max_pages, seq_lens, batch, groups * d, d_rope);
   if (st != LKV_OK) return st;
-  if (static_cast<long long>(batch) * s_q * h_q >= (1LL << 31)) return LKV_ERR_UNSUPPORTED;
+  if (static_cast<long long>(batch) * s_q * h_q >= (1LL << 28)) return LKV_ERR_UNSUPPORTED;
   int num_sms;
-  unsigned long long wait_ns;
-  if ((st = lkv_internal_device_info(&p.err, &num_sms, &wait_ns)) != LKV_OK) return st;
-  if (!workspace || !al(workspace, 16) ||
-      workspace_bytes < lkv_paged_decode_workspace_size(batch, s_q, h_q, groups, d, num_sms))
-    return LKV_ERR_WORKSPACE;
+  if ((st = lkv_internal_device_info(&p.err, &num_sms, &p.wait_limit_ns)) != LKV_OK) return st;
+  PagedPlan w;
+  paged_plan(&w, s_q, h_q, groups, d, num_sms);
+  if (!workspace || !al(workspace, 16) || workspace_bytes < w.total) return LKV_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_rope = static_cast<const __nv_bfloat16*>(q_rope);
   p.B = batch;
@@ -201,13 +275,18 @@ lkv_status lkv_paged_decode_int4(const void* q, const void* q_rope, const void* 
   p.h_q = h_q;
   p.G = groups;
   p.hpg = h_q / groups;
-  p.d = d;
-  p.d_rope = d_rope;
-  p.scale = scale;
+  p.R = s_q * p.hpg;
+  p.RB = w.RB;
+  p.U = w.U;
+  p.P = w.P;
+  p.lockstep = w.lockstep;
+  p.sl2 = scale * 1.4426950408889634f;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
-  paged_decode_kernel<<<static_cast<unsigned>(batch) * s_q * h_q, kPagedThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  return launched();
+  p.seg_info = reinterpret_cast<int*>(ws + w.seg);
+  p.part_lse = reinterpret_cast<float*>(ws + w.lse);
+  p.part_o = reinterpret_cast<float*>(ws + w.o);
+  return launch_decode_for(p, d, w.N, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

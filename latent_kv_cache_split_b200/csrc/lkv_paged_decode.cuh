@@ -1,5 +1,27 @@
 // Decode attention over paged 4-bit cache rows (lkv_int4.cuh): the tied forms, where the state of a
-// group is its key (with the shared RoPE key) and its value.
+// group (D columns of the latent) is its key, with the shared RoPE key, and its value.
+//
+// A unit is a block of at most N query rows (heads of one group times new tokens) of one request.  The
+// products are taken with the keys in the MMA's M dimension, since a unit has few rows:
+//   S^T[key, row] = K[key, :] . Q[row, :]          M = 128 keys, N rows, K = D + 64 columns
+//   O^T[c, row]  += V^T[c, key] . P^T[key, row]    M = 128 value columns (D / 128 blocks), N rows, K = 128 keys
+// A 128-key tile costs (D + 64) / 16 + D / 16 MMAs, and at N <= 64 each takes about 46 cycles to issue
+// whatever N is (measured with one issuing thread; 40 with two), so rows come almost free up to 64.
+//
+// 4-bit codes are no operand of these MMAs, so four converter warps turn each tile into bf16 in shared
+// memory, exactly: (word >> 4i) & 0x000f000f | 0x43004300 is a pair of bf16 128 + u, and one fma by the
+// scale s with -136 s (17 x 4 bits: exact) leaves (u - 8) s.  Rows without a token become zeros, so
+// nothing behind a request's end reaches an MMA.  The next tile's codes, scales and RoPE keys are in
+// flight in registers while this one is converted, its page numbers one tile earlier still.
+//
+// Softmax in the exp2 domain against a reference per row instead of the running maximum: the first
+// tile's maximum, raised only when some score passes it by 2^64 (fp32 sums and bf16 weights have the
+// range, and a weight's relative precision does not depend on it).  A tile then needs no reduction over
+// its keys, only a vote of the eight softmax warps on whether any score passed.
+//
+// Warps: 0 QK issuer and TMEM owner, 1 PV issuer, 4-11 softmax and epilogue (warp w: TMEM lane quadrant
+// w % 4, rows N/2 * h .. with h = (w - 4) / 4; a thread owns one key of the tile, or one value column of
+// O^T), 12-15 converters (32 keys of the tile each).
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -8,90 +30,785 @@
 
 namespace lkv {
 
+constexpr int kPagedThreads = 512;
+constexpr int kPagedTile = 128;
+constexpr float kPagedRaise = 64.f;  // log2 units a score may pass its row's reference by
+
 struct PagedDecodeParams {
   Paged pages;
-  const __nv_bfloat16* q;       // [B, s_q, h_q, d]
-  const __nv_bfloat16* q_rope;  // [B, s_q, h_q, d_rope]
-  int B, s_q, h_q, G, hpg, d, d_rope;
-  float scale;
-  __nv_bfloat16* out;  // [B, s_q, h_q, d]
+  const __nv_bfloat16* q;       // [B, s_q, h_q, D]
+  const __nv_bfloat16* q_rope;  // [B, s_q, h_q, 64]
+  int B, s_q, h_q, G, hpg;
+  int R;         // rows of a group: s_q * hpg
+  int RB;        // row blocks of a group
+  int U;         // units of a request: G * RB
+  int P;         // ranges (CTAs)
+  int lockstep;  // the U units of a request run on neighbouring CTAs at the same pace
+  float sl2;     // scale * log2(e)
+  __nv_bfloat16* out;  // [B, s_q, h_q, D]
   float* lse;          // [B, s_q, h_q]
+  int* seg_info;       // [2P] 4 * unit + (1: holds the unit's first tile) + (2: its last); -1: no partial
+  float* part_lse;     // [2P][N]
+  float* part_o;       // [2P][N][D]
   int* err;
+  unsigned long long wait_limit_ns;
 };
 
-constexpr int kPagedThreads = 128;
-constexpr int kPagedChunk = 128;
-constexpr int kPagedMaxD = 512;
+// ------------------------------------------------------------------------------------------
+// Work partition.  The tiles of all units are laid end to end (request-major) and cut into P equal
+// ranges; in lockstep the requests' tiles are cut into P / U blocks, and range p walks block p / U for
+// unit p % U, so that the units of a request read its RoPE keys and scales from L2.  A range is walked
+// as segments, the runs of its tiles that belong to one unit; a segment that is not a whole unit leaves
+// a partial (slot 0 the range's first segment, 1 its last).
+// ------------------------------------------------------------------------------------------
+struct PagedSegment {
+  int b, unit, group, row0;  // unit = b * U + u; row0: the unit's first row in its group
+  int L, tile_lo, tile_hi;
+  int first, last;           // holds the unit's first / last tile
+  int slot;                  // partial slot; -1 where the segment is the whole unit
+};
 
-__device__ __forceinline__ float int4_at(const uint8_t* row, int r, int c) {
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(row + (c / 8) * 4);
-  const int e = c % 8;
-  const int u = (w >> (4 * (e / 2) + 16 * (e & 1))) & 15;
-  return static_cast<float>(u - 8) * __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row + r / 2)[c / kInt4Block]);
+struct PagedCursor {
+  long long t_begin, t_end, t0;  // t0: the first tile of unit (b, u)
+  int b, u, produced;
+
+  __device__ __forceinline__ bool next(const PagedDecodeParams& p, int rows, PagedSegment& s) {
+    while (b < p.B && t0 < t_end) {
+      const int L = max(0, __ldg(p.pages.seq_lens + b));
+      const int nt = (L + kPagedTile - 1) / kPagedTile;
+      const long long lo = t_begin > t0 ? t_begin - t0 : 0;
+      const long long hi = t_end - t0 < nt ? t_end - t0 : nt;
+      const int cb = b, cu = u;
+      t0 += nt;
+      if (p.lockstep || ++u == p.U) {
+        if (!p.lockstep) u = 0;
+        ++b;
+      }
+      if (hi <= lo) continue;
+      s.b = cb;
+      s.unit = cb * p.U + cu;
+      s.group = cu / p.RB;
+      s.row0 = (cu - s.group * p.RB) * rows;
+      s.L = L;
+      s.tile_lo = static_cast<int>(lo);
+      s.tile_hi = static_cast<int>(hi);
+      s.first = lo == 0;
+      s.last = hi == nt;
+      s.slot = s.first && s.last ? -1 : (produced == 0 ? 0 : 1);
+      ++produced;
+      return true;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ long long paged_tiles(const PagedDecodeParams& p, int b) {
+  return b < p.B ? (max(0, __ldg(p.pages.seq_lens + b)) + kPagedTile - 1) / kPagedTile : 0;
 }
 
-// One CTA per (request, query token, head), keys in chunks with a running maximum and sum.
-__global__ void __launch_bounds__(kPagedThreads) paged_decode_kernel(const PagedDecodeParams p) {
-  __shared__ float qs[kPagedMaxD + 256];
-  __shared__ float ps[kPagedChunk];
-  __shared__ long long at[kPagedChunk];
-  __shared__ float red[kPagedThreads / 32];
-  const int h = blockIdx.x % p.h_q, i = (blockIdx.x / p.h_q) % p.s_q, b = blockIdx.x / (p.h_q * p.s_q);
-  const int j = h / p.hpg, tid = threadIdx.x, r = p.G * p.d;
-  const int nvis = max(0, __ldg(p.pages.seq_lens + b)) - p.s_q + i + 1;
-  const size_t qrow = (static_cast<size_t>(b) * p.s_q + i) * p.h_q + h;
-  for (int c = tid; c < p.d; c += kPagedThreads) qs[c] = __bfloat162float(p.q[qrow * p.d + c]);
-  for (int c = tid; c < p.d_rope; c += kPagedThreads) qs[p.d + c] = __bfloat162float(p.q_rope[qrow * p.d_rope + c]);
-  float acc[kPagedMaxD / kPagedThreads] = {};
-  float m = -INFINITY, l = 0.f;
-  for (int t0 = 0; t0 < nvis; t0 += kPagedChunk) {
-    const int n = min(kPagedChunk, nvis - t0);
-    __syncthreads();
-    float s = -INFINITY;
-    if (tid < n) {
-      at[tid] = paged_row(p.pages, b, t0 + tid);
-      if (at[tid] < 0) record_error(p.err, LKV_SITE_BAD_ROW);
-      s = 0.f;
-      if (at[tid] >= 0) {
-        const uint8_t* row = p.pages.pool + at[tid];
-        for (int c = 0; c < p.d; ++c) s = fmaf(qs[c], int4_at(row, r, j * p.d + c), s);
-        const __nv_bfloat16* kr = reinterpret_cast<const __nv_bfloat16*>(row + int4_rope_at(r));
-        for (int c = 0; c < p.d_rope; ++c) s = fmaf(qs[p.d + c], __bfloat162float(kr[c]), s);
+// Start of range `range`; called by one full warp.
+__device__ __forceinline__ PagedCursor paged_locate(const PagedDecodeParams& p, int range, int lane) {
+  const int mult = p.lockstep ? 1 : p.U;
+  long long total = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) total += paged_tiles(p, b0 + lane);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  total *= mult;
+  const int n = p.lockstep ? p.P / p.U : p.P, k = p.lockstep ? range / p.U : range;
+  PagedCursor c;
+  c.t_begin = total * k / n;
+  c.t_end = total * (k + 1) / n;
+  c.produced = 0;
+  c.u = p.lockstep ? range % p.U : 0;
+  c.b = p.B;
+  c.t0 = total;
+  long long acc = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const long long t = paged_tiles(p, b0 + lane) * mult;
+    long long incl = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, acc + incl > c.t_begin);
+    if (hit) {
+      const int l0 = __ffs(hit) - 1;
+      c.b = b0 + l0;
+      c.t0 = acc + __shfl_sync(0xffffffffu, incl - t, l0);
+      const long long per = __shfl_sync(0xffffffffu, t, l0) / mult;
+      if (!p.lockstep) {
+        c.u = static_cast<int>((c.t_begin - c.t0) / per);
+        c.t0 += c.u * per;
       }
-      s *= p.scale;
+      break;
     }
-    float mx = s;
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if ((tid & 31) == 0) red[tid >> 5] = mx;
-    __syncthreads();
-    const float mn = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float alpha = m == -INFINITY ? 0.f : expf(m - mn);
-    const float e = tid < n ? expf(s - mn) : 0.f;
-    ps[tid] = e;
-    float sum = e;
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    __syncthreads();
-    if ((tid & 31) == 0) red[tid >> 5] = sum;
-    __syncthreads();
-    l = l * alpha + ((red[0] + red[1]) + (red[2] + red[3]));
-    m = mn;
+    acc += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return c;
+}
+
+// ------------------------------------------------------------------------------------------
+template <int D, int N>
+struct PagedCfg {
+  static constexpr int kBox = kPagedTile * 128;  // 128 keys x 64 bf16, 128-byte swizzle
+  static constexpr int kKBoxes = D / 64;
+  static constexpr int kStage = (kKBoxes + 1) * kBox;  // the state, then the RoPE key
+  static constexpr int kStages = D == 128 ? 3 : D == 256 ? 2 : 1;
+  static constexpr int kQBox = N * 128;
+  static constexpr int kQBytes = (kKBoxes + 1) * kQBox;
+  static constexpr int kPBytes = kPagedTile * N * 2;
+  static constexpr int kPs = D == 256 && N == 64 ? 1 : 2;  // P buffers: two where they fit
+  static constexpr int kRW = N / 2;                        // rows of a softmax warp
+  static constexpr int kMB = D / 128;                      // M blocks of PV
+  static constexpr uint32_t kO0 = 2 * N;                   // TMEM: two S^T buffers, then O^T
+  static constexpr int kTmemNeed = 2 * N + kMB * N;
+  static constexpr int kTmemCols = kTmemNeed <= 64 ? 64 : kTmemNeed <= 128 ? 128 : 256;
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage + kQBytes + kPs * kPBytes;
+  static_assert(kTmemNeed <= 256, "TMEM budget");
+  static_assert(kSmem <= 232448 - 8192, "shared memory budget");
+};
+
+constexpr int kPagedSite = LKV_SITE_WAIT_BASE + 300;  // wait sites of this kernel
+enum PagedWaitSite { PW_EMPTY = 1, PW_FULL, PW_SFREE, PW_QREADY, PW_PFULL, PW_OFREE, PW_SFULL, PW_ODONE, PW_VOTE, PW_XCHG, PW_DRAIN };
+
+template <int N>
+struct __align__(16) PagedSmem {
+  uint64_t full[3], empty[3];
+  uint64_t s_full[2], s_free[2], p_full[2], o_done[2];
+  uint64_t q_ready, o_free, drain, vote_bar, xchg_bar;
+  alignas(16) float red[2][8][N / 2];  // [buffer][softmax warp][row of its half]
+  alignas(16) float ref[8][N / 2];     // per warp: its rows' references (log2 units)
+  alignas(16) float fac[8][N / 2];     // per warp: rescale factors, then 1 / l
+  uint32_t vote[3];
+  uint32_t tmem_base, abort;
+  PagedCursor cur;
+};
+
+template <int RW>
+__device__ __forceinline__ void tmem_load_rows(uint32_t taddr, float (&v)[RW]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  if constexpr (RW == 32) {
+    tmem_ld32(taddr, reinterpret_cast<uint32_t(&)[32]>(*r));
+  } else if constexpr (RW == 16) {
+    tmem_ld16(taddr, reinterpret_cast<uint32_t(&)[16]>(*r));
+  } else {
+    tmem_ld8(taddr, reinterpret_cast<uint32_t(&)[8]>(*r));
+  }
+}
+template <int RW>
+__device__ __forceinline__ void tmem_store_rows(uint32_t taddr, const float (&v)[RW]) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+  if constexpr (RW == 32) {
+    tmem_st32(taddr, reinterpret_cast<const uint32_t(&)[32]>(*r));
+  } else if constexpr (RW == 16) {
+    tmem_st16(taddr, reinterpret_cast<const uint32_t(&)[16]>(*r));
+  } else {
+    tmem_st8(taddr, reinterpret_cast<const uint32_t(&)[8]>(*r));
+  }
+}
+
+// Reduce RW values (rows) of every lane over the warp's lanes: lane l ends with row l % RW.
+template <bool kMax, int RW>
+__device__ __forceinline__ float paged_rows_reduce(float (&v)[RW], int lane) {
 #pragma unroll
-    for (int a = 0; a < kPagedMaxD / kPagedThreads; ++a) {
-      const int c = tid + a * kPagedThreads;
-      if (c >= p.d) continue;
-      float o = 0.f;
-      for (int t = 0; t < n; ++t)
-        if (at[t] >= 0) o = fmaf(ps[t], int4_at(p.pages.pool + at[t], r, j * p.d + c), o);
-      acc[a] = acc[a] * alpha + o;
+  for (int s = RW / 2; s >= 1; s >>= 1) {
+    const bool up = (lane & s) != 0;
+#pragma unroll
+    for (int j = 0; j < s; ++j) {
+      const float got = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + s], s);
+      const float keep = up ? v[j + s] : v[j];
+      v[j] = kMax ? fmaxf(keep, got) : keep + got;
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  float x = v[0];
 #pragma unroll
-  for (int a = 0; a < kPagedMaxD / kPagedThreads; ++a) {
-    const int c = tid + a * kPagedThreads;
-    if (c < p.d) p.out[qrow * p.d + c] = __float2bfloat16_rn(acc[a] * inv);
+  for (int s = RW; s < 32; s <<= 1) {
+    const float got = __shfl_xor_sync(0xffffffffu, x, s);
+    x = kMax ? fmaxf(x, got) : x + got;
   }
-  if (tid == 0) p.lse[qrow] = l > 0.f ? m + logf(l) : -INFINITY;
+  return x;
+}
+
+// Eight codes times their scale: bf16 pairs of columns (2i, 2i + 1).
+__device__ __forceinline__ uint4 int4_expand(uint32_t w, __nv_bfloat162 s, __nv_bfloat162 off) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t u = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    __nv_bfloat162 v = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&u), s, off);
+    o[i] = *reinterpret_cast<uint32_t*>(&v);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int D, int N>
+__global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
+  using Cfg = PagedCfg<D, N>;
+  constexpr int TN = kPagedTile, KS = Cfg::kStages, PS = Cfg::kPs, RW = Cfg::kRW;
+  constexpr int kBox = Cfg::kBox;
+  constexpr uint32_t O0 = Cfg::kO0;
+  constexpr int SB = kPagedSite;
+
+  extern __shared__ __align__(1024) uint8_t paged_smem_raw[];
+  __shared__ PagedSmem<N> sm;
+  uint8_t* dsm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(paged_smem_raw) + 1023) &
+                                            ~static_cast<uintptr_t>(1023));
+  uint8_t* qsm = dsm + KS * Cfg::kStage;
+  uint8_t* psm = qsm + Cfg::kQBytes;
+  const uint32_t stage_base = smem_u32(dsm), q_base = smem_u32(qsm), p_base = smem_u32(psm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int range = blockIdx.x;
+
+  if (tid == 0) {
+    for (int s = 0; s < 3; ++s) {
+      mbar_init(smem_u32(&sm.full[s]), 4);  // the converter warps
+      mbar_init(smem_u32(&sm.empty[s]), 1);
+      sm.vote[s] = 0;
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&sm.s_full[b]), 1);
+      mbar_init(smem_u32(&sm.s_free[b]), 8);  // the softmax warps
+      mbar_init(smem_u32(&sm.p_full[b]), 8);
+      mbar_init(smem_u32(&sm.o_done[b]), 1);
+    }
+    mbar_init(smem_u32(&sm.q_ready), 8);
+    mbar_init(smem_u32(&sm.o_free), 8);
+    mbar_init(smem_u32(&sm.vote_bar), 8);
+    mbar_init(smem_u32(&sm.xchg_bar), 8);
+    mbar_init(smem_u32(&sm.drain), 2);  // one commit from each issuer
+    sm.abort = 0;
+    p.seg_info[2 * range] = -1;
+    p.seg_info[2 * range + 1] = -1;
+    fence_mbar_init();
+  }
+  if (warp == 4) {
+    const PagedCursor c = paged_locate(p, range, lane);
+    if (lane == 0) sm.cur = c;
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(&sm.tmem_base), Cfg::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid == 0) griddep_launch_dependents();  // the combine may start launching
+  const uint32_t tbase = sm.tmem_base;
+  const WaitCtl wc{&sm.abort, p.err, p.wait_limit_ns};
+  PagedCursor cur = sm.cur;
+  PagedSegment sg;
+  auto wait_all = [&](uint64_t& bar, int phase, int site) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), static_cast<uint32_t>(phase & 1), wc, SB + site)) != 0;
+  };
+  auto warp_arrive = [&](uint64_t& bar) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bar));
+  };
+
+  if (warp < 2) {
+    // ================================================================== MMA issuers
+    if (lane == 0) {
+      int n = 0, seg = 0;
+      bool ok = true;
+      if (warp == 0) {
+        // A = the key tile, B = Q, both K-major
+        const uint32_t id = idesc_bf16(128, N, 0, 0);
+        const uint64_t qdesc = sdesc_sw128(q_base, 16, 1024);
+        while (ok && cur.next(p, N, sg)) {
+          for (int t = sg.tile_lo; t < sg.tile_hi; ++t, ++n) {
+            const int st = n % KS, sb = n & 1;
+            if (!mbar_wait(smem_u32(&sm.full[st]), static_cast<uint32_t>((n / KS) & 1), wc, SB + PW_FULL) ||
+                (n >= 2 && !mbar_wait(smem_u32(&sm.s_free[sb]), static_cast<uint32_t>(((n - 2) >> 1) & 1), wc, SB + PW_SFREE)) ||
+                (t == sg.tile_lo && !mbar_wait(smem_u32(&sm.q_ready), static_cast<uint32_t>(seg & 1), wc, SB + PW_QREADY))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t kdesc = sdesc_sw128(stage_base + st * Cfg::kStage, 16, 1024);
+#pragma unroll
+            for (int ks = 0; ks < (D + 64) / 16; ++ks)
+              umma_ss(tbase + N * sb, desc_add(kdesc, (ks >> 2) * kBox + (ks & 3) * 32),
+                      desc_add(qdesc, (ks >> 2) * Cfg::kQBox + (ks & 3) * 32), id, ks ? 1u : 0u);
+            umma_commit(smem_u32(&sm.s_full[sb]));
+          }
+          ++seg;
+        }
+      } else {
+        // A = the same tile read MN-major (two 64-column boxes an M block, LBO between them), B = P^T,
+        // MN-major: 8-key atoms of 8 * 2N bytes, swizzled over the 2N bytes of a key's rows
+        const uint32_t id = idesc_bf16(128, N, 1, 1);
+        constexpr uint32_t atom = 16 * N;
+        while (ok && cur.next(p, N, sg)) {
+          for (int t = sg.tile_lo; t < sg.tile_hi; ++t, ++n) {
+            const int pb = n % PS;
+            const bool first = t == sg.tile_lo;
+            if (!mbar_wait(smem_u32(&sm.p_full[pb]), static_cast<uint32_t>((n / PS) & 1), wc, SB + PW_PFULL) ||
+                (first && seg > 0 && !mbar_wait(smem_u32(&sm.o_free), static_cast<uint32_t>((seg - 1) & 1), wc, SB + PW_OFREE))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t paddr = p_base + pb * Cfg::kPBytes;
+            const uint64_t pdesc = N == 64 ? sdesc_sw128(paddr, 16, atom) : N == 32 ? sdesc_sw64(paddr, 16, atom) : sdesc_sw32(paddr, 16, atom);
+#pragma unroll
+            for (int mb = 0; mb < Cfg::kMB; ++mb) {
+              const uint64_t vdesc = sdesc_sw128(stage_base + (n % KS) * Cfg::kStage + 2 * mb * kBox, kBox, 1024);
+#pragma unroll
+              for (int kk = 0; kk < TN / 16; ++kk)
+                umma_ss(tbase + O0 + N * mb, desc_add(vdesc, kk * 2048), desc_add(pdesc, kk * 2 * atom), id,
+                        first && kk == 0 ? 0u : 1u);
+            }
+            umma_commit(smem_u32(&sm.o_done[pb]));
+            umma_commit(smem_u32(&sm.empty[n % KS]));
+          }
+          ++seg;
+        }
+      }
+      // every MMA of this thread is complete before TMEM is released (both issuers arrive)
+      umma_commit(smem_u32(&sm.drain));
+      uint32_t zero = 0;
+      const WaitCtl dc{&zero, p.err, p.wait_limit_ns};
+      mbar_wait(smem_u32(&sm.drain), 0, dc, SB + PW_DRAIN);
+    }
+  } else if (warp >= 12) {
+    // ================================================================== converters
+    // Warp w takes keys 32 w .. 32 w + 31 of each tile.  A lane takes the rows lane % 8 + 8 k and, of each, the
+    // 32-column chunks lane / 8 + 4 h: eight lanes then write eight different 16-byte columns of the swizzled
+    // rows (no bank conflicts), and a warp's load covers whole sectors of eight rows.
+    constexpr int kBatch = D == 512 ? 16 : 32;  // rows of the warp held in registers at once
+    constexpr int kK = kBatch / 8, kB = 32 / kBatch, kH = D / 128;
+    const int w = warp - 12, rl = lane & 7, cl = lane >> 3;
+    const int r = p.G * D;
+    const uint8_t* pool = p.pages.pool;
+    const int rope_at = int4_rope_at(r) + 16 * cl;
+    struct Tile {
+      int b, t, L, group;
+    };
+    PagedSegment walk;
+    int walk_t = 0, walk_hi = 0;
+    auto next_tile = [&](Tile& x) -> bool {
+      if (walk_t >= walk_hi) {
+        if (!cur.next(p, N, walk)) return false;
+        walk_t = walk.tile_lo;
+        walk_hi = walk.tile_hi;
+      }
+      x = Tile{walk.b, walk_t++, walk.L, walk.group};
+      return true;
+    };
+    // this lane's key of a tile: its page, asked for a tile before it is needed
+    int page = -1, slot = 0;
+    bool key_live = false, on_table = false;
+    auto ask_page = [&](const Tile& x) {
+      const int key = x.t * TN + 32 * w + lane;
+      key_live = key < x.L;
+      const int k = key / p.pages.page_size;
+      slot = key - k * p.pages.page_size;
+      on_table = key_live && k < p.pages.max_pages;
+      page = on_table ? __ldg(p.pages.table + x.b * p.pages.table_stride + k) : -1;
+    };
+    auto row_of_page = [&]() -> long long {
+      if (page >= 0 && page < p.pages.n_pages) return page * p.pages.page_stride + slot * p.pages.row_stride;
+      if (key_live) record_error(p.err, LKV_SITE_BAD_ROW);
+      return -1;
+    };
+    uint4 code[kK][kH], key[kK][2];
+    uint32_t scale[kK][kH];
+    auto load_row = [&](long long off, int batch, int group, int k) {
+      const long long at = __shfl_sync(0xffffffffu, off, batch * kBatch + 8 * k + rl);
+      const uint8_t* row = pool + at;
+#pragma unroll
+      for (int h = 0; h < kH; ++h) {
+        code[k][h] = make_uint4(0u, 0u, 0u, 0u);
+        scale[k][h] = 0;
+        if (at >= 0) {
+          const int c = group * (D / 32) + cl + 4 * h;
+          code[k][h] = __ldg(reinterpret_cast<const uint4*>(row) + c);
+          scale[k][h] = __ldg(reinterpret_cast<const unsigned short*>(row + r / 2) + c);
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        key[k][h] = make_uint4(0u, 0u, 0u, 0u);
+        if (at >= 0) key[k][h] = __ldg(reinterpret_cast<const uint4*>(row + rope_at + 64 * h));
+      }
+    };
+    Tile now, then, later;
+    bool have = next_tile(now);
+    bool have_then = false, have_later = false;
+    long long off = -1, off_then = -1;
+    if (have) {
+      ask_page(now);
+      off = row_of_page();
+#pragma unroll
+      for (int k = 0; k < kK; ++k) load_row(off, 0, now.group, k);
+      have_then = next_tile(then);
+      if (have_then) ask_page(then);
+    }
+    for (int n = 0; have; ++n) {
+      off_then = -1;
+      if (have_then) {
+        off_then = row_of_page();
+        have_later = next_tile(later);
+        if (have_later) ask_page(later);
+      } else {
+        then = now;
+        have_later = false;
+      }
+      const int st = n % KS;
+      if (n >= KS && !wait_all(sm.empty[st], n / KS - 1, PW_EMPTY)) break;
+      uint8_t* stage = dsm + st * Cfg::kStage;
+#pragma unroll
+      for (int bt = 0; bt < kB; ++bt) {
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+          uint8_t* dst = stage + (32 * w + bt * kBatch + 8 * k + rl) * 128;
+#pragma unroll
+          for (int h = 0; h < kH; ++h) {
+            const int c = cl + 4 * h;
+            const uint32_t s2 = scale[k][h] * 0x10001u;
+            const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&s2);
+            const __nv_bfloat162 o = __hmul2(s, __float2bfloat162_rn(-136.f));
+            const uint32_t word[4] = {code[k][h].x, code[k][h].y, code[k][h].z, code[k][h].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              *reinterpret_cast<uint4*>(dst + (c >> 1) * kBox + (((4 * (c & 1) + e) ^ rl) << 4)) = int4_expand(word[e], s, o);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<uint4*>(dst + Cfg::kKBoxes * kBox + (((cl + 4 * h) ^ rl) << 4)) = key[k][h];
+          if (bt + 1 < kB)
+            load_row(off, bt + 1, now.group, k);
+          else
+            load_row(off_then, 0, then.group, k);
+        }
+      }
+      fence_proxy_async_smem();
+      warp_arrive(sm.full[st]);
+      now = then;
+      then = later;
+      off = off_then;
+      have = have_then;
+      have_then = have_later;
+    }
+  } else if (warp >= 4) {
+    // ================================================================== softmax / epilogue
+    const int sw = warp - 4;
+    const int q4 = warp & 3;                   // TMEM lane quadrant
+    const int hh = sw >> 2, rb = RW * hh;      // rows rb .. rb + RW - 1 of the unit
+    const int k = q4 * 32 + lane;              // key of the tile; value column (of an M block) of O^T
+    const int rl = lane % RW;                  // this lane's row, rb + rl, after a reduction over lanes
+    const uint32_t tlane = tbase + (static_cast<uint32_t>(q4 * 32) << 16);
+    int xc = 0, vc = 0;
+    // every warp posts one value per row (lanes 0 .. RW - 1) and reads the posts of the 4 warps with its rows
+    auto exchange = [&](float v, float (&all)[4]) -> bool {
+      const int b = xc & 1;
+      if (lane < RW) sm.red[b][sw][lane] = v;
+      warp_arrive(sm.xchg_bar);
+      const bool okx = wait_all(sm.xchg_bar, xc, PW_XCHG);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) all[w] = sm.red[b][4 * hh + w][rl];
+      ++xc;
+      return okx;
+    };
+    // the unit's Q as the K-major B operand, rows behind the group's last as zeros
+    auto load_q = [&](const PagedSegment& s) {
+      constexpr int kC = (D + 64) / 8;
+      for (int idx = sw * 32 + lane; idx < N * kC; idx += 256) {
+        const int row = idx / kC, c = idx % kC;
+        const int bx = c >> 3, cc = c & 7, g = s.row0 + row;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (g < p.R) {
+          const int i = g >= p.hpg;
+          const size_t qrow = (static_cast<size_t>(s.b) * p.s_q + i) * p.h_q + s.group * p.hpg + (g - i * p.hpg);
+          x = bx < Cfg::kKBoxes ? __ldg(reinterpret_cast<const uint4*>(p.q + qrow * D + 64 * bx) + cc)
+                                : __ldg(reinterpret_cast<const uint4*>(p.q_rope + qrow * 64) + cc);
+        }
+        *reinterpret_cast<uint4*>(qsm + bx * Cfg::kQBox + row * 128 + ((cc ^ (row & 7)) << 4)) = x;
+      }
+      fence_proxy_async_smem();
+      warp_arrive(sm.q_ready);
+    };
+
+    // idle requests: no tile is walked for them
+    for (int b = range; b < p.B; b += p.P) {
+      if (__ldg(p.pages.seq_lens + b) > 0) continue;
+      const size_t rows = static_cast<size_t>(p.s_q) * p.h_q;
+      uint4* o = reinterpret_cast<uint4*>(p.out + b * rows * D);
+      for (size_t e = sw * 32 + lane; e < rows * D / 8; e += 256) o[e] = make_uint4(0u, 0u, 0u, 0u);
+      for (size_t e = sw * 32 + lane; e < rows; e += 256) p.lse[b * rows + e] = -INFINITY;
+    }
+
+    PagedSegment nx;
+    bool ok = true;
+    int n = 0;
+    float m_run = 0.f;  // reference of row rb + rl (log2 units)
+    float l[RW];        // this key lane's share of each row's sum of weights
+    bool have = cur.next(p, N, sg);
+    if (have) load_q(sg);
+    while (ok && have) {
+      bool have_nx = false;
+      const int lim0 = sg.L - p.s_q;  // query i sees keys 0 .. lim0 + i
+      for (int t = sg.tile_lo; t < sg.tile_hi; ++t, ++n) {
+        const int sb = n & 1, pb = n % PS;
+        const bool first = t == sg.tile_lo;
+        if (!wait_all(sm.s_full[sb], n >> 1, PW_SFULL)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float x[RW];
+        tmem_load_rows<RW>(tlane + N * sb + rb, x);
+        tmem_wait_ld();
+        tc_fence_before();
+        warp_arrive(sm.s_free[sb]);
+        if (t == sg.tile_hi - 1 && (have_nx = cur.next(p, N, nx))) load_q(nx);  // this unit's QKs are done
+        if ((t + 1) * TN - 1 > lim0) {
+          const int kg = t * TN + k;
+#pragma unroll
+          for (int j = 0; j < RW; ++j)
+            if (kg > lim0 + (sg.row0 + rb + j >= p.hpg ? 1 : 0)) x[j] = -INFINITY;
+        }
+        bool raise = first;
+        if (!first) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int j4 = 0; j4 < RW / 4; ++j4) {
+            const float4 r4 = reinterpret_cast<const float4*>(sm.ref[sw])[j4];
+            x[4 * j4] = fmaf(x[4 * j4], p.sl2, -r4.x);
+            x[4 * j4 + 1] = fmaf(x[4 * j4 + 1], p.sl2, -r4.y);
+            x[4 * j4 + 2] = fmaf(x[4 * j4 + 2], p.sl2, -r4.z);
+            x[4 * j4 + 3] = fmaf(x[4 * j4 + 3], p.sl2, -r4.w);
+            top = fmaxf(top, fmaxf(fmaxf(x[4 * j4], x[4 * j4 + 1]), fmaxf(x[4 * j4 + 2], x[4 * j4 + 3])));
+          }
+          // The flag of vote vc is one of three words: it is cleared after vote vc + 1, when every warp has read
+          // it, and set again for vote vc + 3 by warps that passed vote vc + 2, which this warp joins after clearing.
+          if (__any_sync(0xffffffffu, top > kPagedRaise) && lane == 0) *const_cast<volatile uint32_t*>(&sm.vote[vc % 3]) = 1u;
+          warp_arrive(sm.vote_bar);
+          if (!wait_all(sm.vote_bar, vc, PW_VOTE)) {
+            ok = false;
+            break;
+          }
+          raise = *const_cast<volatile uint32_t*>(&sm.vote[vc % 3]) != 0;
+          if (sw == 0 && lane == 0) *const_cast<volatile uint32_t*>(&sm.vote[(vc + 2) % 3]) = 0u;
+          ++vc;
+        }
+        if (raise) {  // the same for all eight warps
+          float mx[RW];
+#pragma unroll
+          for (int j = 0; j < RW; ++j) {
+            x[j] = first ? x[j] * p.sl2 : x[j] + sm.ref[sw][j];
+            mx[j] = x[j];
+          }
+          const float mw = paged_rows_reduce<true, RW>(mx, lane);
+          float all[4];
+          if (!exchange(mw, all)) {
+            ok = false;
+            break;
+          }
+          const float mt = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
+          // a row that sees no key of the segment's first tile sees none of its later ones
+          const float m_new = first ? (mt == -INFINITY ? 0.f : mt) : fmaxf(m_run, mt);
+          __syncwarp();
+          if (lane < RW) {
+            sm.ref[sw][lane] = m_new;
+            sm.fac[sw][lane] = first ? 1.f : ex2_approx(m_run - m_new);
+          }
+          m_run = m_new;
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < RW; ++j) {
+            x[j] -= sm.ref[sw][j];
+            l[j] = first ? 0.f : l[j] * sm.fac[sw][j];
+          }
+        }
+        uint32_t pw[RW / 2];
+#pragma unroll
+        for (int j = 0; j < RW / 2; ++j) {
+          const float e0 = ex2_approx(x[2 * j]), e1 = ex2_approx(x[2 * j + 1]);
+          l[2 * j] += e0;
+          l[2 * j + 1] += e1;
+          pw[j] = pack_bf16x2(e0, e1);
+        }
+        // P buffer pb was last read by PV(n - PS)
+        if (n >= PS && !wait_all(sm.o_done[pb], n / PS - 1, PW_ODONE)) {
+          ok = false;
+          break;
+        }
+        {
+          // a key's rows are 2N bytes; 16-byte chunk c lies at c ^ the swizzle of that width
+          uint8_t* prow = psm + pb * Cfg::kPBytes + k * (2 * N);
+          const int x8 = N == 64 ? (k & 7) : N == 32 ? ((k >> 1) & 3) : ((k >> 2) & 1);
+#pragma unroll
+          for (int c = 0; c < RW / 8; ++c)
+            *reinterpret_cast<uint4*>(prow + (((hh * (RW / 8) + c) ^ x8) << 4)) =
+                make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
+        }
+        fence_proxy_async_smem();
+        if (raise && !first) {
+          // O^T holds the segment's tiles up to n - 1
+          if (!wait_all(sm.o_done[(n - 1) % PS], (n - 1) / PS, PW_ODONE)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int mb = 0; mb < Cfg::kMB; ++mb) {
+            float o[RW];
+            tmem_load_rows<RW>(tlane + O0 + N * mb + rb, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < RW; ++j) o[j] *= sm.fac[sw][j];
+            tmem_store_rows<RW>(tlane + O0 + N * mb + rb, o);
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        warp_arrive(sm.p_full[pb]);
+        if (t != sg.tile_hi - 1) continue;
+        // ---------------------------------------------------------------- the segment's end
+        const float lw = paged_rows_reduce<false, RW>(l, lane);
+        float lt[4];
+        if (!exchange(lw, lt)) {
+          ok = false;
+          break;
+        }
+        const float lsum = (lt[0] + lt[1]) + (lt[2] + lt[3]);
+        // a NaN sum stays NaN in both results
+        const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+        const float lse = lsum == 0.f ? -INFINITY : (m_run + log2f(lsum)) * 0.69314718055994531f;
+        __syncwarp();
+        if (lane < RW) sm.fac[sw][lane] = inv;
+        __syncwarp();
+        if (!wait_all(sm.o_done[pb], n / PS, PW_ODONE)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const size_t part = static_cast<size_t>(2 * range + (sg.slot < 0 ? 0 : sg.slot)) * N;
+        const size_t out0 = static_cast<size_t>(sg.b) * p.s_q * p.h_q + sg.group * p.hpg;
+#pragma unroll
+        for (int mb = 0; mb < Cfg::kMB; ++mb) {
+          float o[RW];
+          tmem_load_rows<RW>(tlane + O0 + N * mb + rb, o);
+          tmem_wait_ld();
+          const int c = 128 * mb + k;
+#pragma unroll
+          for (int j = 0; j < RW; ++j) {
+            const int g = sg.row0 + rb + j;
+            if (g >= p.R) continue;
+            const float v = o[j] * sm.fac[sw][j];
+            if (sg.slot < 0) {
+              const int i = g >= p.hpg;
+              p.out[(out0 + static_cast<size_t>(i) * p.h_q + (g - i * p.hpg)) * D + c] = __float2bfloat16_rn(v);
+            } else {
+              p.part_o[(part + rb + j) * D + c] = v;
+            }
+          }
+        }
+        if (q4 == 0 && lane < RW) {
+          const int g = sg.row0 + rb + lane;
+          if (g < p.R) {
+            const int i = g >= p.hpg;
+            if (sg.slot < 0)
+              p.lse[out0 + static_cast<size_t>(i) * p.h_q + (g - i * p.hpg)] = lse;
+            else
+              p.part_lse[part + rb + lane] = lse;
+          }
+        }
+        if (sg.slot >= 0 && sw == 0 && lane == 0) p.seg_info[2 * range + sg.slot] = 4 * sg.unit + sg.first + 2 * sg.last;
+        tc_fence_before();
+        warp_arrive(sm.o_free);
+      }
+      if (!ok) break;
+      have = have_nx;
+      if (have) sg = nx;
+    }
+  }
+  // ---------------------------------------------------------------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tbase, Cfg::kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// Join the partials of the units that ranges share.  Block (p, y): if range p holds the first tile of such a
+// unit, its pieces are that slot and slot 0 of the following ranges (of the same lockstep unit) up to the one
+// with the last tile; a warp joins one row,
+//   lse = ln sum_k exp(lse_k),  out = sum_k exp(lse_k - lse) o_k,  in range order.
+// ------------------------------------------------------------------------------------------
+constexpr int kPagedCombineWarps = 8;
+constexpr int kPagedMaxRanges = 1024;
+
+template <int D, int N>
+__global__ void __launch_bounds__(kPagedCombineWarps * 32) paged_combine_kernel(const __grid_constant__ PagedDecodeParams p) {
+  __shared__ int piece[kPagedMaxRanges];
+  __shared__ int n_pieces, unit;
+  griddep_wait();  // a programmatic dependent of the decode kernel: its writes first
+  const int range = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  if (tid == 0) {
+    n_pieces = 0;
+    for (int slot = 0; slot < 2; ++slot) {
+      const int s = p.seg_info[2 * range + slot];
+      if (s < 0 || (s & 3) != 1) continue;
+      unit = s >> 2;
+      piece[0] = 2 * range + slot;
+      int n = 1;
+      const int step = p.lockstep ? p.U : 1;
+      for (int q = range + step; q < p.P; q += step) {
+        const int v = p.seg_info[2 * q];
+        if (v < 0) continue;  // a range without tiles
+        if ((v >> 2) != unit) break;
+        piece[n++] = 2 * q;
+        if (v & 2) break;
+      }
+      n_pieces = n;
+    }
+  }
+  __syncthreads();
+  const int n = n_pieces;
+  if (n == 0) return;
+  const int row = blockIdx.y * kPagedCombineWarps + (tid >> 5);
+  const int b = unit / p.U, u = unit - b * p.U, group = u / p.RB;
+  const int g = (u - group * p.RB) * N + row;
+  if (row >= N || g >= p.R) return;
+  float mx = -INFINITY;
+  for (int k = lane; k < n; k += 32) mx = fmaxf(mx, p.part_lse[static_cast<size_t>(piece[k]) * N + row]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float top = mx == -INFINITY ? 0.f : mx;
+  float tot = 0.f;
+  float4 acc[D / 128];
+#pragma unroll
+  for (int c = 0; c < D / 128; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int k = 0; k < n; ++k) {
+    const size_t at = static_cast<size_t>(piece[k]) * N + row;
+    const float w = expf(p.part_lse[at] - top);  // 0 for a piece whose keys the row does not see
+    tot += w;
+#pragma unroll
+    for (int c = 0; c < D / 128; ++c) {
+      const float4 o = *reinterpret_cast<const float4*>(p.part_o + at * D + 128 * c + 4 * lane);
+      acc[c].x = fmaf(w, o.x, acc[c].x);
+      acc[c].y = fmaf(w, o.y, acc[c].y);
+      acc[c].z = fmaf(w, o.z, acc[c].z);
+      acc[c].w = fmaf(w, o.w, acc[c].w);
+    }
+  }
+  const float inv = tot == 0.f ? 0.f : 1.f / tot;
+  const int i = g >= p.hpg;
+  const size_t orow = (static_cast<size_t>(b) * p.s_q + i) * p.h_q + group * p.hpg + (g - i * p.hpg);
+#pragma unroll
+  for (int c = 0; c < D / 128; ++c) {
+    uint2 v;
+    v.x = pack_bf16x2(acc[c].x * inv, acc[c].y * inv);
+    v.y = pack_bf16x2(acc[c].z * inv, acc[c].w * inv);
+    *reinterpret_cast<uint2*>(p.out + orow * D + 128 * c + 4 * lane) = v;
+  }
+  if (lane == 0) p.lse[orow] = tot == 0.f ? -INFINITY : top + logf(tot);
 }
 
 }  // namespace lkv
