@@ -29,7 +29,7 @@ struct Paged {
   uint8_t* pool;
   long long page_stride, row_stride;  // bytes
   long long n_pages;
-  int page_size;
+  int page_size, page_shift;  // page_shift: log2 of page_size, or -1 where it is no power of two
   const int* table;  // [batch, max_pages], row stride table_stride
   long long table_stride;
   int max_pages;

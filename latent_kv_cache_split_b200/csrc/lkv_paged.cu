@@ -48,6 +48,9 @@ lkv_status check_pool(Paged* g, const void* pool, int64_t page_stride, int64_t r
   g->row_stride = row_stride;
   g->n_pages = n_pages;
   g->page_size = page_size;
+  g->page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (page_size == 1 << i) g->page_shift = i;
   g->table = table;
   g->table_stride = table_stride;
   g->max_pages = max_pages;
@@ -108,7 +111,7 @@ lkv_status launch_decode(const PagedDecodeParams& p, cudaStream_t s) {
     }
     ready[dev] = true;
   }
-  paged_decode_kernel<D, N><<<p.P, kPagedThreads, Cfg::kSmem, s>>>(p);
+  paged_decode_kernel<D, N><<<p.P, Cfg::kThreads, Cfg::kSmem, s>>>(p);
   const lkv_status st = launched();
   if (st != LKV_OK) return st;
   cudaLaunchConfig_t cfg = {};

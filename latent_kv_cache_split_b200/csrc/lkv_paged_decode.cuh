@@ -8,29 +8,29 @@
 // A 128-key tile costs (D + 64) / 16 + D / 16 MMAs, and at N <= 64 each takes about 46 cycles to issue
 // whatever N is (measured with one issuing thread; 40 with two), so rows come almost free up to 64.
 //
-// 4-bit codes are no operand of these MMAs, so four converter warps turn each tile into bf16 in shared
+// 4-bit codes are no operand of these MMAs, so converter warps turn each tile into bf16 in shared
 // memory, exactly: (word >> 4i) & 0x000f000f | 0x43004300 is a pair of bf16 128 + u, and one fma by the
 // scale s with -136 s (17 x 4 bits: exact) leaves (u - 8) s.  Rows without a token become zeros, so
-// nothing behind a request's end reaches an MMA.  The next tile's codes, scales and RoPE keys are in
-// flight in registers while this one is converted, its page numbers one tile earlier still.
+// nothing behind a request's end reaches an MMA.
 //
 // Softmax in the exp2 domain against a reference per row instead of the running maximum: the first
 // tile's maximum, raised only when some score passes it by 2^64 (fp32 sums and bf16 weights have the
 // range, and a weight's relative precision does not depend on it).  A tile then needs no reduction over
-// its keys, only a vote of the eight softmax warps on whether any score passed.
+// its keys, only a vote of the softmax warps on whether any score passed.
 //
-// Warps: 0 QK issuer and TMEM owner, 1 PV issuer, 4-11 softmax and epilogue (warp w: TMEM lane quadrant
-// w % 4, rows N/2 * h .. with h = (w - 4) / 4; a thread owns one key of the tile, or one value column of
-// O^T), 12-15 converters (32 keys of the tile each).
+// Warps: 0 QK issuer and TMEM owner, 1 PV issuer, from 4 on softmax and epilogue (warp w: TMEM lane quadrant
+// w % 4; a thread owns one key of the tile, or one value column of O^T), then the converters, in groups
+// that take turns at the tiles.
 #pragma once
 #include <cstdint>
+#include <utility>
 #include <cuda_bf16.h>
 #include "lkv_int4.cuh"
 #include "lkv_ptx.cuh"
 
 namespace lkv {
 
-constexpr int kPagedThreads = 512;
+constexpr int kPagedConv = 8;  // converter warps
 constexpr int kPagedTile = 128;
 constexpr float kPagedRaise = 64.f;  // log2 units a score may pass its row's reference by
 
@@ -155,11 +155,21 @@ struct PagedCfg {
   static constexpr int kKBoxes = D / 64;
   static constexpr int kStage = (kKBoxes + 1) * kBox;  // the state, then the RoPE key
   static constexpr int kStages = D == 128 ? 3 : D == 256 ? 2 : 1;
+  // Converter warps of a tile; the others take the next one.  Turns need two stages: a group that waits for a
+  // stage's release must find the release before it complete, which the order of the tiles gives it then.
+  static constexpr int kTileWarps = kStages > 1 ? kPagedConv / 2 : kPagedConv;
+  static constexpr int kTurns = kPagedConv / kTileWarps;
+  static constexpr int kWarpKeys = kPagedTile / kTileWarps;
   static constexpr int kQBox = N * 128;
   static constexpr int kQBytes = (kKBoxes + 1) * kQBox;
   static constexpr int kPBytes = kPagedTile * N * 2;
   static constexpr int kPs = D == 256 && N == 64 ? 1 : 2;  // P buffers: two where they fit
-  static constexpr int kRW = N / 2;                        // rows of a softmax warp
+  // Softmax warps: four, one for each TMEM lane quadrant, with all N rows (a warp's waits and arrivals cost about as
+  // much as 16 rows do); 64 rows are split between two such sets, for their registers.
+  static constexpr int kSW = N == 64 ? 8 : 4;
+  static constexpr int kRW = 4 * N / kSW;                  // rows of a softmax warp
+  static constexpr int kConv0 = 4 + kSW;                   // first converter warp
+  static constexpr int kThreads = 32 * (kConv0 + kPagedConv);
   static constexpr int kMB = D / 128;                      // M blocks of PV
   static constexpr uint32_t kO0 = 2 * N;                   // TMEM: two S^T buffers, then O^T
   static constexpr int kTmemNeed = 2 * N + kMB * N;
@@ -172,18 +182,29 @@ struct PagedCfg {
 constexpr int kPagedSite = LKV_SITE_WAIT_BASE + 300;  // wait sites of this kernel
 enum PagedWaitSite { PW_EMPTY = 1, PW_FULL, PW_SFREE, PW_QREADY, PW_PFULL, PW_OFREE, PW_SFULL, PW_ODONE, PW_VOTE, PW_XCHG, PW_DRAIN };
 
-template <int N>
+template <int RW, int SW>
 struct __align__(16) PagedSmem {
   uint64_t full[3], empty[3];
   uint64_t s_full[2], s_free[2], p_full[2], o_done[2];
   uint64_t q_ready, o_free, drain, vote_bar, xchg_bar;
-  alignas(16) float red[2][8][N / 2];  // [buffer][softmax warp][row of its half]
-  alignas(16) float ref[8][N / 2];     // per warp: its rows' references (log2 units)
-  alignas(16) float fac[8][N / 2];     // per warp: rescale factors, then 1 / l
+  alignas(16) float red[2][SW][RW];  // [buffer][softmax warp][its row]
+  alignas(16) float ref[SW][RW];     // per warp: its rows' references (log2 units)
+  alignas(16) float fac[SW][RW];     // per warp: rescale factors, then 1 / l
   uint32_t vote[3];
   uint32_t tmem_base, abort;
   PagedCursor cur;
+  // Walk state of the warps that run out of registers first: read where it is needed.
+  PagedCursor walk[SW + kPagedConv];
+  PagedSegment seg[SW][2], conv_seg[kPagedConv];
 };
+
+// The next segment of a warp's own walk, both in shared memory; the same answer in every lane.
+__device__ __noinline__ bool paged_next(const PagedDecodeParams& p, int rows, PagedCursor& walk, PagedSegment& out, int lane) {
+  int ok = 0;
+  __syncwarp();
+  if (lane == 0) ok = walk.next(p, rows, out);
+  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
 
 template <int RW>
 __device__ __forceinline__ void tmem_load_rows(uint32_t taddr, float (&v)[RW]) {
@@ -230,52 +251,161 @@ __device__ __forceinline__ float paged_rows_reduce(float (&v)[RW], int lane) {
   return x;
 }
 
-// Eight codes times their scale: bf16 pairs of columns (2i, 2i + 1).
-__device__ __forceinline__ uint4 int4_expand(uint32_t w, __nv_bfloat162 s, __nv_bfloat162 off) {
+// Loads at a constant offset.  Volatile: the compiler keeps them where they are, ahead of the waits that their
+// latency is to overlap.  The _if forms give zeros where `ok` is 0.
+template <int kAt>
+__device__ __forceinline__ uint4 ldg16(const uint8_t* ptr) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4+%5];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(ptr), "n"(kAt));
+  return v;
+}
+template <int kAt>
+__device__ __forceinline__ uint32_t ldg2(const uint8_t* ptr) {
+  uint32_t v;
+  asm volatile("{\n\t.reg .u16 h;\n\tld.global.nc.u16 h, [%1+%2];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "l"(ptr), "n"(kAt));
+  return v;
+}
+template <int kAt>
+__device__ __forceinline__ uint4 ldg16_if(const uint8_t* ptr, bool ok) {
+  return ok ? ldg16<kAt>(ptr) : make_uint4(0u, 0u, 0u, 0u);
+}
+template <int kAt>
+__device__ __forceinline__ uint32_t ldg2_if(const uint8_t* ptr, bool ok) {
+  return ok ? ldg2<kAt>(ptr) : 0u;
+}
+__device__ __forceinline__ void prefetch_l2(const uint8_t* ptr) { asm volatile("prefetch.global.L2 [%0];" ::"l"(ptr)); }
+
+template <class F, int... I>
+__device__ __forceinline__ void static_for_of(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int kN, class F>
+__device__ __forceinline__ void static_for(F&& f) {
+  static_for_of(f, std::make_integer_sequence<int, kN>{});
+}
+
+// Eight codes times their scale: bf16 pairs of columns (2i, 2i + 1).  mask and magic are 0x000f000f and 0x43004300
+// in registers, so that one lop3 takes both.
+__device__ __forceinline__ uint4 int4_expand(uint32_t w, uint32_t mask, uint32_t magic, __nv_bfloat162 s, __nv_bfloat162 off) {
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t u = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    uint32_t u;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(u) : "r"(w >> (4 * i)), "r"(mask), "r"(magic));
     __nv_bfloat162 v = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&u), s, off);
     o[i] = *reinterpret_cast<uint32_t*>(&v);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// ------------------------------------------------------------------------------------------
+// The softmax warps' rare work, out of line: inlined, its registers spilled the loop's over every tile (a spill's
+// reload misses an L1 that streams codes, and cost the loop more than half of its time).
+// ------------------------------------------------------------------------------------------
+// A segment's Q as the K-major B operand, rows behind the group's last as zeros.
+template <int D, int N, int kThreads>
+__device__ __noinline__ void paged_load_q(const PagedDecodeParams& p, const PagedSegment& s, uint8_t* qsm, int first) {
+  constexpr int kC = (D + 64) / 8;
+#pragma unroll 2
+  for (int idx = first; idx < N * kC; idx += kThreads) {
+    const int row = idx / kC, c = idx % kC;
+    const int bx = c >> 3, cc = c & 7, g = s.row0 + row;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (g < p.R) {
+      const int i = g >= p.hpg;
+      const size_t qrow = (static_cast<size_t>(s.b) * p.s_q + i) * p.h_q + s.group * p.hpg + (g - i * p.hpg);
+      x = bx < D / 64 ? __ldg(reinterpret_cast<const uint4*>(p.q + qrow * D + 64 * bx) + cc)
+                      : __ldg(reinterpret_cast<const uint4*>(p.q_rope + qrow * 64) + cc);
+    }
+    *reinterpret_cast<uint4*>(qsm + bx * (N * 128) + row * 128 + ((cc ^ (row & 7)) << 4)) = x;
+  }
+  fence_proxy_async_smem();
+}
+
+// The largest score of row lane % RW over the warp's 32 keys; scores at `ahead` > limit are not seen.
+template <int RW>
+__device__ __noinline__ float paged_find_max(uint32_t tmem, int ahead, int newest, int lane) {
+  float x[RW];
+  tmem_load_rows<RW>(tmem, x);
+  tmem_wait_ld();
+#pragma unroll
+  for (int j = 0; j < RW; ++j)
+    if (ahead > (j >= newest ? 1 : 0)) x[j] = -INFINITY;
+  return paged_rows_reduce<true, RW>(x, lane);
+}
+
+// O^T times the rows' factors.
+template <int RW, int N, int kMB>
+__device__ __noinline__ void paged_rescale(uint32_t tmem, const float* fac) {
+#pragma unroll 1
+  for (int mb = 0; mb < kMB; ++mb) {
+    float o[RW];
+    tmem_load_rows<RW>(tmem + N * mb, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < RW; ++j) o[j] *= fac[j];
+    tmem_store_rows<RW>(tmem + N * mb, o);
+  }
+  tmem_wait_st();
+}
+
+// O^T times 1 / l: the result, or the range's partial.  c: this thread's value column of each M block.
+template <int D, int N, int RW, int kMB>
+__device__ __noinline__ void paged_store_out(const PagedDecodeParams& p, const PagedSegment& s, uint32_t tmem, const float* inv, int rb,
+                                             int c, size_t part) {
+  const int n = min(RW, p.R - (s.row0 + rb));
+#pragma unroll 1
+  for (int mb = 0; mb < kMB; ++mb, c += 128) {
+    float o[RW];
+    tmem_load_rows<RW>(tmem + N * mb, o);
+    tmem_wait_ld();
+    const size_t row0 = static_cast<size_t>(s.b) * p.s_q * p.h_q + s.group * p.hpg;
+#pragma unroll
+    for (int j = 0; j < RW; ++j) {
+      if (j >= n) break;
+      const int g = s.row0 + rb + j;
+      const float v = o[j] * inv[j];
+      if (s.slot < 0)
+        p.out[(row0 + (g >= p.hpg ? p.h_q + g - p.hpg : g)) * D + c] = __float2bfloat16_rn(v);
+      else
+        p.part_o[(part + rb + j) * D + c] = v;
+    }
+  }
+}
+
 template <int D, int N>
-__global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
+__global__ void __launch_bounds__(PagedCfg<D, N>::kThreads, 1) paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
   using Cfg = PagedCfg<D, N>;
-  constexpr int TN = kPagedTile, KS = Cfg::kStages, PS = Cfg::kPs, RW = Cfg::kRW;
+  constexpr int TN = kPagedTile, KS = Cfg::kStages, PS = Cfg::kPs, RW = Cfg::kRW, SW = Cfg::kSW;
   constexpr int kBox = Cfg::kBox;
   constexpr uint32_t O0 = Cfg::kO0;
   constexpr int SB = kPagedSite;
 
   extern __shared__ __align__(1024) uint8_t paged_smem_raw[];
-  __shared__ PagedSmem<N> sm;
-  uint8_t* dsm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(paged_smem_raw) + 1023) &
-                                            ~static_cast<uintptr_t>(1023));
+  __shared__ PagedSmem<RW, SW> sm;
+  uint8_t* dsm = paged_smem_raw + ((1024u - (smem_u32(paged_smem_raw) & 1023u)) & 1023u);
   uint8_t* qsm = dsm + KS * Cfg::kStage;
   uint8_t* psm = qsm + Cfg::kQBytes;
   const uint32_t stage_base = smem_u32(dsm), q_base = smem_u32(qsm), p_base = smem_u32(psm);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int range = blockIdx.x;
 
   if (tid == 0) {
     for (int s = 0; s < 3; ++s) {
-      mbar_init(smem_u32(&sm.full[s]), 4);  // the converter warps
+      mbar_init(smem_u32(&sm.full[s]), Cfg::kTileWarps);
       mbar_init(smem_u32(&sm.empty[s]), 1);
       sm.vote[s] = 0;
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&sm.s_full[b]), 1);
-      mbar_init(smem_u32(&sm.s_free[b]), 8);  // the softmax warps
-      mbar_init(smem_u32(&sm.p_full[b]), 8);
+      mbar_init(smem_u32(&sm.s_free[b]), SW);  // the softmax warps
+      mbar_init(smem_u32(&sm.p_full[b]), SW);
       mbar_init(smem_u32(&sm.o_done[b]), 1);
     }
-    mbar_init(smem_u32(&sm.q_ready), 8);
-    mbar_init(smem_u32(&sm.o_free), 8);
-    mbar_init(smem_u32(&sm.vote_bar), 8);
-    mbar_init(smem_u32(&sm.xchg_bar), 8);
+    mbar_init(smem_u32(&sm.q_ready), SW);
+    mbar_init(smem_u32(&sm.o_free), SW);
+    mbar_init(smem_u32(&sm.vote_bar), SW);
+    mbar_init(smem_u32(&sm.xchg_bar), SW);
     mbar_init(smem_u32(&sm.drain), 2);  // one commit from each issuer
     sm.abort = 0;
     p.seg_info[2 * range] = -1;
@@ -296,8 +426,6 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
   if (tid == 0) griddep_launch_dependents();  // the combine may start launching
   const uint32_t tbase = sm.tmem_base;
   const WaitCtl wc{&sm.abort, p.err, p.wait_limit_ns};
-  PagedCursor cur = sm.cur;
-  PagedSegment sg;
   auto wait_all = [&](uint64_t& bar, int phase, int site) -> bool {
     return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), static_cast<uint32_t>(phase & 1), wc, SB + site)) != 0;
   };
@@ -308,7 +436,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
 
   if (warp < 2) {
     // ================================================================== MMA issuers
-    if (lane == 0) {
+    if (elect_one()) {
+      PagedCursor cur = sm.cur;
+      PagedSegment sg;
       int n = 0, seg = 0;
       bool ok = true;
       if (warp == 0) {
@@ -371,125 +501,128 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
       const WaitCtl dc{&zero, p.err, p.wait_limit_ns};
       mbar_wait(smem_u32(&sm.drain), 0, dc, SB + PW_DRAIN);
     }
-  } else if (warp >= 12) {
+  } else if (warp >= Cfg::kConv0) {
     // ================================================================== converters
-    // Warp w takes keys 32 w .. 32 w + 31 of each tile.  A lane takes the rows lane % 8 + 8 k and, of each, the
-    // 32-column chunks lane / 8 + 4 h: eight lanes then write eight different 16-byte columns of the swizzled
-    // rows (no bank conflicts), and a warp's load covers whole sectors of eight rows.
-    constexpr int kBatch = D == 512 ? 16 : 32;  // rows of the warp held in registers at once
-    constexpr int kK = kBatch / 8, kB = 32 / kBatch, kH = D / 128;
-    const int w = warp - 12, rl = lane & 7, cl = lane >> 3;
+    // A group of kTileWarps takes every kTurns-th tile, warp w of it kWarpKeys keys of the tile.  A lane takes the rows lane % 8 + 8 k and, of each, the 32-column chunks lane / 8 + 4 h: eight lanes then write eight
+    // different 16-byte columns of the swizzled rows (no bank conflicts), and a warp's load covers whole sectors of
+    // eight rows.  A tile's rows are asked into L2 while the group converts the tile before it, and their page numbers
+    // one tile earlier still; while one group waits for its loads another converts.
+    constexpr int kKeys = Cfg::kWarpKeys, kK = kKeys / 8, kH = D / 128;
+    const int w = (warp - Cfg::kConv0) % Cfg::kTileWarps, rl = lane & 7, cl = lane >> 3;
     const int r = p.G * D;
     const uint8_t* pool = p.pages.pool;
-    const int rope_at = int4_rope_at(r) + 16 * cl;
+    const int key_at = int4_rope_at(r);
     struct Tile {
-      int b, t, L, group;
+      int b, t, L, group;  // t < 0: none
     };
-    PagedSegment walk;
+    PagedCursor& walk = sm.walk[SW + warp - Cfg::kConv0];
+    PagedSegment& seg = sm.conv_seg[warp - Cfg::kConv0];
+    if (lane == 0) walk = sm.cur;
     int walk_t = 0, walk_hi = 0;
-    auto next_tile = [&](Tile& x) -> bool {
-      if (walk_t >= walk_hi) {
-        if (!cur.next(p, N, walk)) return false;
-        walk_t = walk.tile_lo;
-        walk_hi = walk.tile_hi;
+    auto next_tile = [&](int skip) -> Tile {
+      for (;; --skip) {
+        if (walk_t >= walk_hi) {
+          if (!paged_next(p, N, walk, seg, lane)) return Tile{0, -1, 0, 0};
+          walk_t = seg.tile_lo;
+          walk_hi = seg.tile_hi;
+        }
+        if (skip == 0) return Tile{seg.b, walk_t++, seg.L, seg.group};
+        ++walk_t;
       }
-      x = Tile{walk.b, walk_t++, walk.L, walk.group};
-      return true;
     };
-    // this lane's key of a tile: its page, asked for a tile before it is needed
+    // this lane's key of a tile: the page is asked for here, used a tile later
     int page = -1, slot = 0;
-    bool key_live = false, on_table = false;
+    bool key_live = false;
     auto ask_page = [&](const Tile& x) {
-      const int key = x.t * TN + 32 * w + lane;
-      key_live = key < x.L;
-      const int k = key / p.pages.page_size;
-      slot = key - k * p.pages.page_size;
-      on_table = key_live && k < p.pages.max_pages;
-      page = on_table ? __ldg(p.pages.table + x.b * p.pages.table_stride + k) : -1;
+      const int key = x.t * TN + kKeys * w + lane;
+      key_live = x.t >= 0 && lane < kKeys && key < x.L;
+      page = -1;
+      if (key_live) {
+        const int k = p.pages.page_shift >= 0 ? key >> p.pages.page_shift : key / p.pages.page_size;
+        slot = key - k * p.pages.page_size;
+        if (k < p.pages.max_pages) page = __ldg(p.pages.table + x.b * p.pages.table_stride + k);
+      }
     };
-    auto row_of_page = [&]() -> long long {
-      if (page >= 0 && page < p.pages.n_pages) return page * p.pages.page_stride + slot * p.pages.row_stride;
-      if (key_live) record_error(p.err, LKV_SITE_BAD_ROW);
-      return -1;
+    auto row_of_page = [&](const Tile& x) -> long long {
+      if (!key_live) return -1;
+      if (page < 0 || page >= p.pages.n_pages) {
+        record_error(p.err, LKV_SITE_BAD_ROW);
+        return -1;
+      }
+      const long long off = page * p.pages.page_stride + slot * p.pages.row_stride;
+      const uint8_t* row = pool + off;
+      prefetch_l2(row + x.group * (D / 2));
+      if (D == 512) prefetch_l2(row + x.group * (D / 2) + 128);
+      prefetch_l2(row + key_at);
+      return off;
     };
     uint4 code[kK][kH], key[kK][2];
     uint32_t scale[kK][kH];
-    auto load_row = [&](long long off, int batch, int group, int k) {
-      const long long at = __shfl_sync(0xffffffffu, off, batch * kBatch + 8 * k + rl);
-      const uint8_t* row = pool + at;
+    auto load_rows = [&](long long off, int group) {
+      const uint8_t* cp = pool + 16 * cl + group * (D / 2);
+      const uint8_t* sp = pool + 2 * cl + r / 2 + group * (D / 16);
+      const uint8_t* kp = pool + 16 * cl + key_at;
+      auto row = [&](int k) { return __shfl_sync(0xffffffffu, off, 8 * k + rl); };
+      if (__all_sync(0xffffffffu, off >= 0 || lane >= kKeys)) {
 #pragma unroll
-      for (int h = 0; h < kH; ++h) {
-        code[k][h] = make_uint4(0u, 0u, 0u, 0u);
-        scale[k][h] = 0;
-        if (at >= 0) {
-          const int c = group * (D / 32) + cl + 4 * h;
-          code[k][h] = __ldg(reinterpret_cast<const uint4*>(row) + c);
-          scale[k][h] = __ldg(reinterpret_cast<const unsigned short*>(row + r / 2) + c);
+        for (int k = 0; k < kK; ++k) {
+          const long long at = row(k);
+          static_for<kH>([&](auto h) { code[k][h] = ldg16<64 * h>(cp + at); });
+          static_for<kH>([&](auto h) { scale[k][h] = ldg2<8 * h>(sp + at); });
+          static_for<2>([&](auto h) { key[k][h] = ldg16<64 * h>(kp + at); });
+        }
+      } else {  // rows without a token: codes 0 times scale 0, and a key of zeros
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+          const long long at = row(k);
+          static_for<kH>([&](auto h) { code[k][h] = ldg16_if<64 * h>(cp + at, at >= 0); });
+          static_for<kH>([&](auto h) { scale[k][h] = ldg2_if<8 * h>(sp + at, at >= 0); });
+          static_for<2>([&](auto h) { key[k][h] = ldg16_if<64 * h>(kp + at, at >= 0); });
         }
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        key[k][h] = make_uint4(0u, 0u, 0u, 0u);
-        if (at >= 0) key[k][h] = __ldg(reinterpret_cast<const uint4*>(row + rope_at + 64 * h));
-      }
     };
-    Tile now, then, later;
-    bool have = next_tile(now);
-    bool have_then = false, have_later = false;
-    long long off = -1, off_then = -1;
-    if (have) {
-      ask_page(now);
-      off = row_of_page();
+    uint32_t mask = 0x000f000fu, magic = 0x43004300u;
+    asm volatile("" : "+r"(mask), "+r"(magic));
+    // where this lane's 16-byte pieces of a row go: word e of a chunk, and the RoPE key's two
+    uint32_t at_code[4], at_key[2];
 #pragma unroll
-      for (int k = 0; k < kK; ++k) load_row(off, 0, now.group, k);
-      have_then = next_tile(then);
-      if (have_then) ask_page(then);
-    }
-    for (int n = 0; have; ++n) {
-      off_then = -1;
-      if (have_then) {
-        off_then = row_of_page();
-        have_later = next_tile(later);
-        if (have_later) ask_page(later);
-      } else {
-        then = now;
-        have_later = false;
-      }
+    for (int e = 0; e < 4; ++e) at_code[e] = (kKeys * w + rl) * 128 + (cl >> 1) * kBox + (((4 * (cl & 1) + e) ^ rl) << 4);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) at_key[h] = (kKeys * w + rl) * 128 + Cfg::kKBoxes * kBox + (((cl + 4 * h) ^ rl) << 4);
+    int n = (warp - Cfg::kConv0) / Cfg::kTileWarps;
+    Tile now = next_tile(n), then = Tile{0, -1, 0, 0};
+    ask_page(now);
+    long long off = row_of_page(now);
+    if (now.t >= 0) then = next_tile(Cfg::kTurns - 1);
+    ask_page(then);
+    for (; now.t >= 0; n += Cfg::kTurns) {
+      load_rows(off, now.group);
+      const long long off_then = row_of_page(then);
+      const Tile later = then.t >= 0 ? next_tile(Cfg::kTurns - 1) : then;
+      ask_page(later);
       const int st = n % KS;
       if (n >= KS && !wait_all(sm.empty[st], n / KS - 1, PW_EMPTY)) break;
       uint8_t* stage = dsm + st * Cfg::kStage;
 #pragma unroll
-      for (int bt = 0; bt < kB; ++bt) {
+      for (int k = 0; k < kK; ++k) {
 #pragma unroll
-        for (int k = 0; k < kK; ++k) {
-          uint8_t* dst = stage + (32 * w + bt * kBatch + 8 * k + rl) * 128;
+        for (int h = 0; h < kH; ++h) {
+          const uint32_t s2 = __byte_perm(scale[k][h], 0, 0x1010);
+          const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&s2);
+          const __nv_bfloat162 o = __hmul2(s, __float2bfloat162_rn(-136.f));
+          const uint32_t word[4] = {code[k][h].x, code[k][h].y, code[k][h].z, code[k][h].w};
 #pragma unroll
-          for (int h = 0; h < kH; ++h) {
-            const int c = cl + 4 * h;
-            const uint32_t s2 = scale[k][h] * 0x10001u;
-            const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&s2);
-            const __nv_bfloat162 o = __hmul2(s, __float2bfloat162_rn(-136.f));
-            const uint32_t word[4] = {code[k][h].x, code[k][h].y, code[k][h].z, code[k][h].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<uint4*>(dst + (c >> 1) * kBox + (((4 * (c & 1) + e) ^ rl) << 4)) = int4_expand(word[e], s, o);
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<uint4*>(dst + Cfg::kKBoxes * kBox + (((cl + 4 * h) ^ rl) << 4)) = key[k][h];
-          if (bt + 1 < kB)
-            load_row(off, bt + 1, now.group, k);
-          else
-            load_row(off_then, 0, then.group, k);
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<uint4*>(stage + at_code[e] + 2 * h * kBox + 1024 * k) = int4_expand(word[e], mask, magic, s, o);
         }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) *reinterpret_cast<uint4*>(stage + at_key[h] + 1024 * k) = key[k][h];
       }
       fence_proxy_async_smem();
       warp_arrive(sm.full[st]);
       now = then;
       then = later;
       off = off_then;
-      have = have_then;
-      have_then = have_later;
     }
   } else if (warp >= 4) {
     // ================================================================== softmax / epilogue
@@ -500,7 +633,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
     const int rl = lane % RW;                  // this lane's row, rb + rl, after a reduction over lanes
     const uint32_t tlane = tbase + (static_cast<uint32_t>(q4 * 32) << 16);
     int xc = 0, vc = 0;
-    // every warp posts one value per row (lanes 0 .. RW - 1) and reads the posts of the 4 warps with its rows
+    // every warp posts one value per row (lanes 0 .. RW - 1) and reads the posts of the four warps with its rows
     auto exchange = [&](float v, float (&all)[4]) -> bool {
       const int b = xc & 1;
       if (lane < RW) sm.red[b][sw][lane] = v;
@@ -511,22 +644,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
       ++xc;
       return okx;
     };
-    // the unit's Q as the K-major B operand, rows behind the group's last as zeros
     auto load_q = [&](const PagedSegment& s) {
-      constexpr int kC = (D + 64) / 8;
-      for (int idx = sw * 32 + lane; idx < N * kC; idx += 256) {
-        const int row = idx / kC, c = idx % kC;
-        const int bx = c >> 3, cc = c & 7, g = s.row0 + row;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (g < p.R) {
-          const int i = g >= p.hpg;
-          const size_t qrow = (static_cast<size_t>(s.b) * p.s_q + i) * p.h_q + s.group * p.hpg + (g - i * p.hpg);
-          x = bx < Cfg::kKBoxes ? __ldg(reinterpret_cast<const uint4*>(p.q + qrow * D + 64 * bx) + cc)
-                                : __ldg(reinterpret_cast<const uint4*>(p.q_rope + qrow * 64) + cc);
-        }
-        *reinterpret_cast<uint4*>(qsm + bx * Cfg::kQBox + row * 128 + ((cc ^ (row & 7)) << 4)) = x;
-      }
-      fence_proxy_async_smem();
+      paged_load_q<D, N, 32 * SW>(p, s, qsm, sw * 32 + lane);
       warp_arrive(sm.q_ready);
     };
 
@@ -535,42 +654,46 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
       if (__ldg(p.pages.seq_lens + b) > 0) continue;
       const size_t rows = static_cast<size_t>(p.s_q) * p.h_q;
       uint4* o = reinterpret_cast<uint4*>(p.out + b * rows * D);
-      for (size_t e = sw * 32 + lane; e < rows * D / 8; e += 256) o[e] = make_uint4(0u, 0u, 0u, 0u);
-      for (size_t e = sw * 32 + lane; e < rows; e += 256) p.lse[b * rows + e] = -INFINITY;
+      for (size_t e = sw * 32 + lane; e < rows * D / 8; e += 32 * SW) o[e] = make_uint4(0u, 0u, 0u, 0u);
+      for (size_t e = sw * 32 + lane; e < rows; e += 32 * SW) p.lse[b * rows + e] = -INFINITY;
     }
 
-    PagedSegment nx;
+    PagedCursor& walk = sm.walk[sw];
+    if (lane == 0) walk = sm.cur;
     bool ok = true;
-    int n = 0;
+    int n = 0, seg = 0;
     float m_run = 0.f;  // reference of row rb + rl (log2 units)
     float l[RW];        // this key lane's share of each row's sum of weights
-    bool have = cur.next(p, N, sg);
-    if (have) load_q(sg);
-    while (ok && have) {
+    bool have = paged_next(p, N, walk, sm.seg[sw][0], lane);
+    if (have) load_q(sm.seg[sw][0]);
+    for (; ok && have; ++seg) {
+      const PagedSegment& sg = sm.seg[sw][seg & 1];
+      PagedSegment& nx = sm.seg[sw][(seg + 1) & 1];
       bool have_nx = false;
-      const int lim0 = sg.L - p.s_q;  // query i sees keys 0 .. lim0 + i
-      for (int t = sg.tile_lo; t < sg.tile_hi; ++t, ++n) {
+      const int t_lo = sg.tile_lo, t_hi = sg.tile_hi;
+      const int lim0 = sg.L - p.s_q;               // query i sees keys 0 .. lim0 + i
+      const int newest = p.hpg - (sg.row0 + rb);   // rows from here on are query 1's (or padding)
+      for (int t = t_lo; t < t_hi; ++t, ++n) {
         const int sb = n & 1, pb = n % PS;
-        const bool first = t == sg.tile_lo;
+        const bool first = t == t_lo;
         if (!wait_all(sm.s_full[sb], n >> 1, PW_SFULL)) {
           ok = false;
           break;
         }
         tc_fence_after();
+        // the tile's scores, -inf where the row does not see the key
         float x[RW];
-        tmem_load_rows<RW>(tlane + N * sb + rb, x);
-        tmem_wait_ld();
-        tc_fence_before();
-        warp_arrive(sm.s_free[sb]);
-        if (t == sg.tile_hi - 1 && (have_nx = cur.next(p, N, nx))) load_q(nx);  // this unit's QKs are done
-        if ((t + 1) * TN - 1 > lim0) {
-          const int kg = t * TN + k;
+        auto load_scores = [&] {
+          tmem_load_rows<RW>(tlane + N * sb + rb, x);
+          tmem_wait_ld();
+          if ((t + 1) * TN - 1 > lim0) {
+            const int ahead = t * TN + k - lim0;
 #pragma unroll
-          for (int j = 0; j < RW; ++j)
-            if (kg > lim0 + (sg.row0 + rb + j >= p.hpg ? 1 : 0)) x[j] = -INFINITY;
-        }
-        bool raise = first;
-        if (!first) {
+            for (int j = 0; j < RW; ++j)
+              if (ahead > (j >= newest ? 1 : 0)) x[j] = -INFINITY;
+          }
+        };
+        auto sub_reference = [&]() -> float {
           float top = -INFINITY;
 #pragma unroll
           for (int j4 = 0; j4 < RW / 4; ++j4) {
@@ -581,6 +704,36 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
             x[4 * j4 + 3] = fmaf(x[4 * j4 + 3], p.sl2, -r4.w);
             top = fmaxf(top, fmaxf(fmaxf(x[4 * j4], x[4 * j4 + 1]), fmaxf(x[4 * j4 + 2], x[4 * j4 + 3])));
           }
+          return top;
+        };
+        // Take the scores against the references and vote; where there is none yet, or the vote asks for it, find the
+        // tile's maxima, raise the references and take the scores again (a second reading spares a copy of them).
+        enum { kVote, kFind, kTake };
+        int step = first ? kFind : kVote;
+        while (true) {
+          if (step == kFind) {
+            const float mw = paged_find_max<RW>(tlane + N * sb + rb, t * TN + k - lim0, newest, lane);
+            float all[4];
+            if (!exchange(mw, all)) {
+              ok = false;
+              break;
+            }
+            const float mt = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3])) * p.sl2;
+            // a row that sees no key of the segment's first tile sees none of its later ones
+            const float m_new = first ? (mt == -INFINITY ? 0.f : mt) : fmaxf(m_run, mt);
+            if (lane < RW) {
+              sm.ref[sw][lane] = m_new;
+              sm.fac[sw][lane] = first ? 0.f : ex2_approx(m_run - m_new);
+            }
+            m_run = m_new;
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < RW; ++j) l[j] = first ? 0.f : l[j] * sm.fac[sw][j];
+            step = kTake;
+          }
+          load_scores();
+          const float top = sub_reference();
+          if (step == kTake) break;
           // The flag of vote vc is one of three words: it is cleared after vote vc + 1, when every warp has read
           // it, and set again for vote vc + 3 by warps that passed vote vc + 2, which this warp joins after clearing.
           if (__any_sync(0xffffffffu, top > kPagedRaise) && lane == 0) *const_cast<volatile uint32_t*>(&sm.vote[vc % 3]) = 1u;
@@ -589,39 +742,16 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
             ok = false;
             break;
           }
-          raise = *const_cast<volatile uint32_t*>(&sm.vote[vc % 3]) != 0;
+          const bool raise = *const_cast<volatile uint32_t*>(&sm.vote[vc % 3]) != 0;  // the same for all softmax warps
           if (sw == 0 && lane == 0) *const_cast<volatile uint32_t*>(&sm.vote[(vc + 2) % 3]) = 0u;
           ++vc;
+          if (!raise) break;
+          step = kFind;
         }
-        if (raise) {  // the same for all eight warps
-          float mx[RW];
-#pragma unroll
-          for (int j = 0; j < RW; ++j) {
-            x[j] = first ? x[j] * p.sl2 : x[j] + sm.ref[sw][j];
-            mx[j] = x[j];
-          }
-          const float mw = paged_rows_reduce<true, RW>(mx, lane);
-          float all[4];
-          if (!exchange(mw, all)) {
-            ok = false;
-            break;
-          }
-          const float mt = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
-          // a row that sees no key of the segment's first tile sees none of its later ones
-          const float m_new = first ? (mt == -INFINITY ? 0.f : mt) : fmaxf(m_run, mt);
-          __syncwarp();
-          if (lane < RW) {
-            sm.ref[sw][lane] = m_new;
-            sm.fac[sw][lane] = first ? 1.f : ex2_approx(m_run - m_new);
-          }
-          m_run = m_new;
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < RW; ++j) {
-            x[j] -= sm.ref[sw][j];
-            l[j] = first ? 0.f : l[j] * sm.fac[sw][j];
-          }
-        }
+        if (!ok) break;
+        tc_fence_before();
+        warp_arrive(sm.s_free[sb]);
+        if (t == t_hi - 1 && (have_nx = paged_next(p, N, walk, nx, lane))) load_q(nx);  // this unit's QKs are done
         uint32_t pw[RW / 2];
 #pragma unroll
         for (int j = 0; j < RW / 2; ++j) {
@@ -645,27 +775,18 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
                 make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
         }
         fence_proxy_async_smem();
-        if (raise && !first) {
+        if (step == kTake && !first) {
           // O^T holds the segment's tiles up to n - 1
           if (!wait_all(sm.o_done[(n - 1) % PS], (n - 1) / PS, PW_ODONE)) {
             ok = false;
             break;
           }
           tc_fence_after();
-#pragma unroll
-          for (int mb = 0; mb < Cfg::kMB; ++mb) {
-            float o[RW];
-            tmem_load_rows<RW>(tlane + O0 + N * mb + rb, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < RW; ++j) o[j] *= sm.fac[sw][j];
-            tmem_store_rows<RW>(tlane + O0 + N * mb + rb, o);
-          }
-          tmem_wait_st();
+          paged_rescale<RW, N, Cfg::kMB>(tlane + O0 + rb, sm.fac[sw]);
         }
         tc_fence_before();
         warp_arrive(sm.p_full[pb]);
-        if (t != sg.tile_hi - 1) continue;
+        if (t != t_hi - 1) continue;
         // ---------------------------------------------------------------- the segment's end
         const float lw = paged_rows_reduce<false, RW>(l, lane);
         float lt[4];
@@ -686,26 +807,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
         }
         tc_fence_after();
         const size_t part = static_cast<size_t>(2 * range + (sg.slot < 0 ? 0 : sg.slot)) * N;
+        paged_store_out<D, N, RW, Cfg::kMB>(p, sg, tlane + O0 + rb, sm.fac[sw], rb, k, part);
         const size_t out0 = static_cast<size_t>(sg.b) * p.s_q * p.h_q + sg.group * p.hpg;
-#pragma unroll
-        for (int mb = 0; mb < Cfg::kMB; ++mb) {
-          float o[RW];
-          tmem_load_rows<RW>(tlane + O0 + N * mb + rb, o);
-          tmem_wait_ld();
-          const int c = 128 * mb + k;
-#pragma unroll
-          for (int j = 0; j < RW; ++j) {
-            const int g = sg.row0 + rb + j;
-            if (g >= p.R) continue;
-            const float v = o[j] * sm.fac[sw][j];
-            if (sg.slot < 0) {
-              const int i = g >= p.hpg;
-              p.out[(out0 + static_cast<size_t>(i) * p.h_q + (g - i * p.hpg)) * D + c] = __float2bfloat16_rn(v);
-            } else {
-              p.part_o[(part + rb + j) * D + c] = v;
-            }
-          }
-        }
         if (q4 == 0 && lane < RW) {
           const int g = sg.row0 + rb + lane;
           if (g < p.R) {
@@ -720,9 +823,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
         tc_fence_before();
         warp_arrive(sm.o_free);
       }
-      if (!ok) break;
       have = have_nx;
-      if (have) sg = nx;
     }
   }
   // ---------------------------------------------------------------------- teardown

@@ -263,6 +263,15 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_
          | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
 }
 
+// One lane of a converged warp.  Code under it that issues tcgen05.mma compiles without the loops that make each
+// operand uniform, which under `lane == 0` cost 46 cycles an MMA (measured: 9 to 32 with A in TMEM, 40 to 48 with both
+// operands in shared memory, at N = 16 to 64).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // D[tmem] (+)= A[smem desc] * B[smem desc]
 __device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                         uint32_t idesc, uint32_t accumulate) {
