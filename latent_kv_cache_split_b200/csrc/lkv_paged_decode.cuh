@@ -152,44 +152,46 @@ __device__ __forceinline__ PagedCursor paged_locate(const PagedDecodeParams& p, 
 template <int D, int N>
 struct PagedCfg {
   static constexpr int kBox = kPagedTile * 128;  // 128 keys x 64 bf16, 128-byte swizzle
-  static constexpr int kKBoxes = D / 64;
-  static constexpr int kStage = (kKBoxes + 1) * kBox;  // the state, then the RoPE key
-  static constexpr int kStages = D == 128 ? 3 : D == 256 ? 2 : 1;
-  // Converter warps of a tile; the others take the next one.  Turns need two stages: a group that waits for a
-  // stage's release must find the release before it complete, which the order of the tiles gives it then.
-  static constexpr int kTileWarps = kStages > 1 ? kPagedConv / 2 : kPagedConv;
-  static constexpr int kTurns = kPagedConv / kTileWarps;
-  static constexpr int kWarpKeys = kPagedTile / kTileWarps;
+  static constexpr int kVBoxes = D / 64;
+  static constexpr int kVStage = kVBoxes * kBox;  // the state in shared memory: the value operand
+  // QK takes the state from TMEM where that has the columns (an MMA with both operands in shared memory reads 4 KB of
+  // A there, 32 cycles of its bandwidth; from TMEM it runs at the tensor core's rate, 16 cycles at N = 32), else from
+  // the value operand's tile; the RoPE key from TMEM always.
+  static constexpr bool kTS = D <= 256;
+  static constexpr int kKCols = (kTS ? D / 2 : 0) + 32;  // TMEM columns of a key stage
+  static constexpr int kVStages = D == 128 ? 3 : D == 256 ? 2 : 1;
+  static constexpr int kKStages = D == 128 ? 3 : 2;
+  static constexpr int kSBufs = D == 256 && N == 64 ? 1 : 2;  // S^T buffers
+  static constexpr int kPs = D == 512 && N == 64 ? 1 : 2;     // P buffers
   static constexpr int kQBox = N * 128;
-  static constexpr int kQBytes = (kKBoxes + 1) * kQBox;
+  static constexpr int kQBytes = (kVBoxes + 1) * kQBox;
   static constexpr int kPBytes = kPagedTile * N * 2;
-  static constexpr int kPs = D == 256 && N == 64 ? 1 : 2;  // P buffers: two where they fit
   // Softmax warps: four, one for each TMEM lane quadrant, with all N rows (a warp's waits and arrivals cost about as
   // much as 16 rows do); 64 rows are split between two such sets, for their registers.
   static constexpr int kSW = N == 64 ? 8 : 4;
-  static constexpr int kRW = 4 * N / kSW;                  // rows of a softmax warp
-  static constexpr int kConv0 = 4 + kSW;                   // first converter warp
+  static constexpr int kRW = 4 * N / kSW;   // rows of a softmax warp
+  static constexpr int kConv0 = 4 + kSW;    // first converter warp
   static constexpr int kThreads = 32 * (kConv0 + kPagedConv);
-  static constexpr int kMB = D / 128;                      // M blocks of PV
-  static constexpr uint32_t kO0 = 2 * N;                   // TMEM: two S^T buffers, then O^T
-  static constexpr int kTmemNeed = 2 * N + kMB * N;
-  static constexpr int kTmemCols = kTmemNeed <= 64 ? 64 : kTmemNeed <= 128 ? 128 : 256;
-  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kStage + kQBytes + kPs * kPBytes;
-  static_assert(kTmemNeed <= 256, "TMEM budget");
+  static constexpr int kMB = D / 128;       // M blocks of PV
+  static constexpr uint32_t kO0 = kSBufs * N, kK0 = kO0 + kMB * N;  // TMEM: S^T buffers, O^T, key stages
+  static constexpr int kTmemNeed = kK0 + kKStages * kKCols;
+  static constexpr int kTmemCols = kTmemNeed <= 128 ? 128 : kTmemNeed <= 256 ? 256 : 512;
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kVStages) * kVStage + kQBytes + kPs * kPBytes;
+  static_assert(kTmemNeed <= 512, "TMEM budget");
   static_assert(kSmem <= 232448 - 8192, "shared memory budget");
 };
 
 constexpr int kPagedSite = LKV_SITE_WAIT_BASE + 300;  // wait sites of this kernel
-enum PagedWaitSite { PW_EMPTY = 1, PW_FULL, PW_SFREE, PW_QREADY, PW_PFULL, PW_OFREE, PW_SFULL, PW_ODONE, PW_VOTE, PW_XCHG, PW_DRAIN };
+enum PagedWaitSite { PW_KEMPTY = 1, PW_VEMPTY, PW_FULL, PW_SFREE, PW_QREADY, PW_PFULL, PW_OFREE, PW_SFULL, PW_ODONE, PW_VOTE, PW_XCHG, PW_DRAIN };
 
 template <int RW, int SW>
 struct __align__(16) PagedSmem {
-  uint64_t full[3], empty[3];
+  uint64_t full[3], kempty[3], vempty[3];
   uint64_t s_full[2], s_free[2], p_full[2], o_done[2];
   uint64_t q_ready, o_free, drain, vote_bar, xchg_bar;
   alignas(16) float red[2][SW][RW];  // [buffer][softmax warp][its row]
   alignas(16) float ref[SW][RW];     // per warp: its rows' references (log2 units)
-  alignas(16) float fac[SW][RW];     // per warp: rescale factors, then 1 / l
+  alignas(16) float fac[SW][RW];     // per warp: what the references rose by, then 1 / l
   uint32_t vote[3];
   uint32_t tmem_base, abort;
   PagedCursor cur;
@@ -302,48 +304,47 @@ __device__ __forceinline__ uint4 int4_expand(uint32_t w, uint32_t mask, uint32_t
 // The softmax warps' rare work, out of line: inlined, its registers spilled the loop's over every tile (a spill's
 // reload misses an L1 that streams codes, and cost the loop more than half of its time).
 // ------------------------------------------------------------------------------------------
-// A segment's Q as the K-major B operand, rows behind the group's last as zeros.
+// A segment's Q as the K-major B operand, rows behind the group's last as zeros.  16-byte piece j of what the
+// converters put into TMEM holds the column pairs of the four lanes c = 0 .. 3: of a 128-column block, with j = 4e + i,
+// columns 32c + 8 (e ^ (c & 2)) + 2i; of the RoPE key 8c + 2j for j < 4, then 32 + 8c + 2 (j - 4).
 template <int D, int N, int kThreads>
 __device__ __noinline__ void paged_load_q(const PagedDecodeParams& p, const PagedSegment& s, uint8_t* qsm, int first) {
   constexpr int kC = (D + 64) / 8;
 #pragma unroll 2
   for (int idx = first; idx < N * kC; idx += kThreads) {
-    const int row = idx / kC, c = idx % kC;
-    const int bx = c >> 3, cc = c & 7, g = s.row0 + row;
+    const int row = idx / kC, piece = idx % kC;
+    const int bx = piece >> 3, cc = piece & 7, g = s.row0 + row;
     uint4 x = make_uint4(0u, 0u, 0u, 0u);
     if (g < p.R) {
       const int i = g >= p.hpg;
       const size_t qrow = (static_cast<size_t>(s.b) * p.s_q + i) * p.h_q + s.group * p.hpg + (g - i * p.hpg);
-      x = bx < D / 64 ? __ldg(reinterpret_cast<const uint4*>(p.q + qrow * D + 64 * bx) + cc)
-                      : __ldg(reinterpret_cast<const uint4*>(p.q_rope + qrow * 64) + cc);
+      const __nv_bfloat16* q = p.q + qrow * D;
+      if (piece >= D / 8) {
+        const uint32_t* k = reinterpret_cast<const uint32_t*>(p.q_rope + qrow * 64) + (cc < 4 ? cc : 12 + cc);
+        x = make_uint4(__ldg(k), __ldg(k + 4), __ldg(k + 8), __ldg(k + 12));
+      } else if (PagedCfg<D, N>::kTS) {
+        const int j = piece & 15, e = j >> 2;
+        const uint32_t* k = reinterpret_cast<const uint32_t*>(q) + 64 * (piece >> 4) + (j & 3);
+        x = make_uint4(__ldg(k + 4 * e), __ldg(k + 16 + 4 * e), __ldg(k + 32 + 4 * (e ^ 2)), __ldg(k + 48 + 4 * (e ^ 2)));
+      } else {
+        x = __ldg(reinterpret_cast<const uint4*>(q) + piece);
+      }
     }
     *reinterpret_cast<uint4*>(qsm + bx * (N * 128) + row * 128 + ((cc ^ (row & 7)) << 4)) = x;
   }
   fence_proxy_async_smem();
 }
 
-// The largest score of row lane % RW over the warp's 32 keys; scores at `ahead` > limit are not seen.
-template <int RW>
-__device__ __noinline__ float paged_find_max(uint32_t tmem, int ahead, int newest, int lane) {
-  float x[RW];
-  tmem_load_rows<RW>(tmem, x);
-  tmem_wait_ld();
-#pragma unroll
-  for (int j = 0; j < RW; ++j)
-    if (ahead > (j >= newest ? 1 : 0)) x[j] = -INFINITY;
-  return paged_rows_reduce<true, RW>(x, lane);
-}
-
-// O^T times the rows' factors.
+// O^T after its rows' references rose by `up`.
 template <int RW, int N, int kMB>
-__device__ __noinline__ void paged_rescale(uint32_t tmem, const float* fac) {
+__device__ __noinline__ void paged_rescale(uint32_t tmem, const float* up) {
 #pragma unroll 1
   for (int mb = 0; mb < kMB; ++mb) {
     float o[RW];
     tmem_load_rows<RW>(tmem + N * mb, o);
     tmem_wait_ld();
 #pragma unroll
-    for (int j = 0; j < RW; ++j) o[j] *= fac[j];
+    for (int j = 0; j < RW; ++j) o[j] *= ex2_approx(-up[j]);
     tmem_store_rows<RW>(tmem + N * mb, o);
   }
   tmem_wait_st();
@@ -376,24 +377,26 @@ __device__ __noinline__ void paged_store_out(const PagedDecodeParams& p, const P
 template <int D, int N>
 __global__ void __launch_bounds__(PagedCfg<D, N>::kThreads, 1) paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
   using Cfg = PagedCfg<D, N>;
-  constexpr int TN = kPagedTile, KS = Cfg::kStages, PS = Cfg::kPs, RW = Cfg::kRW, SW = Cfg::kSW;
+  constexpr int TN = kPagedTile, VS = Cfg::kVStages, KS = Cfg::kKStages, SS = Cfg::kSBufs, PS = Cfg::kPs;
+  constexpr int RW = Cfg::kRW, SW = Cfg::kSW;
   constexpr int kBox = Cfg::kBox;
-  constexpr uint32_t O0 = Cfg::kO0;
+  constexpr uint32_t O0 = Cfg::kO0, K0 = Cfg::kK0;
   constexpr int SB = kPagedSite;
 
   extern __shared__ __align__(1024) uint8_t paged_smem_raw[];
   __shared__ PagedSmem<RW, SW> sm;
   uint8_t* dsm = paged_smem_raw + ((1024u - (smem_u32(paged_smem_raw) & 1023u)) & 1023u);
-  uint8_t* qsm = dsm + KS * Cfg::kStage;
+  uint8_t* qsm = dsm + VS * Cfg::kVStage;
   uint8_t* psm = qsm + Cfg::kQBytes;
-  const uint32_t stage_base = smem_u32(dsm), q_base = smem_u32(qsm), p_base = smem_u32(psm);
+  const uint32_t v_base = smem_u32(dsm), q_base = smem_u32(qsm), p_base = smem_u32(psm);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int range = blockIdx.x;
 
   if (tid == 0) {
     for (int s = 0; s < 3; ++s) {
-      mbar_init(smem_u32(&sm.full[s]), Cfg::kTileWarps);
-      mbar_init(smem_u32(&sm.empty[s]), 1);
+      mbar_init(smem_u32(&sm.full[s]), kPagedConv);
+      mbar_init(smem_u32(&sm.kempty[s]), 1);
+      mbar_init(smem_u32(&sm.vempty[s]), 1);
       sm.vote[s] = 0;
     }
     for (int b = 0; b < 2; ++b) {
@@ -442,30 +445,36 @@ __global__ void __launch_bounds__(PagedCfg<D, N>::kThreads, 1) paged_decode_kern
       int n = 0, seg = 0;
       bool ok = true;
       if (warp == 0) {
-        // A = the key tile, B = Q, both K-major
+        // A = the key tile (state and RoPE key in TMEM; for D = 512 the state in shared memory), B = Q, K-major
         const uint32_t id = idesc_bf16(128, N, 0, 0);
         const uint64_t qdesc = sdesc_sw128(q_base, 16, 1024);
         while (ok && cur.next(p, N, sg)) {
           for (int t = sg.tile_lo; t < sg.tile_hi; ++t, ++n) {
-            const int st = n % KS, sb = n & 1;
-            if (!mbar_wait(smem_u32(&sm.full[st]), static_cast<uint32_t>((n / KS) & 1), wc, SB + PW_FULL) ||
-                (n >= 2 && !mbar_wait(smem_u32(&sm.s_free[sb]), static_cast<uint32_t>(((n - 2) >> 1) & 1), wc, SB + PW_SFREE)) ||
+            const int sb = n % SS;
+            if (!mbar_wait(smem_u32(&sm.full[n % VS]), static_cast<uint32_t>((n / VS) & 1), wc, SB + PW_FULL) ||
+                (n >= SS && !mbar_wait(smem_u32(&sm.s_free[sb]), static_cast<uint32_t>((n / SS - 1) & 1), wc, SB + PW_SFREE)) ||
                 (t == sg.tile_lo && !mbar_wait(smem_u32(&sm.q_ready), static_cast<uint32_t>(seg & 1), wc, SB + PW_QREADY))) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint64_t kdesc = sdesc_sw128(stage_base + st * Cfg::kStage, 16, 1024);
+            const uint32_t ktm = tbase + K0 + (n % KS) * Cfg::kKCols;
+            const uint64_t kdesc = sdesc_sw128(v_base + (n % VS) * Cfg::kVStage, 16, 1024);
 #pragma unroll
-            for (int ks = 0; ks < (D + 64) / 16; ++ks)
-              umma_ss(tbase + N * sb, desc_add(kdesc, (ks >> 2) * kBox + (ks & 3) * 32),
-                      desc_add(qdesc, (ks >> 2) * Cfg::kQBox + (ks & 3) * 32), id, ks ? 1u : 0u);
+            for (int ks = 0; ks < (D + 64) / 16; ++ks) {
+              const uint64_t qd = desc_add(qdesc, (ks >> 2) * Cfg::kQBox + (ks & 3) * 32);
+              if (Cfg::kTS || ks >= D / 16)
+                umma_ts(tbase + N * sb, ktm + 8 * (Cfg::kTS ? ks : ks - D / 16), qd, id, ks ? 1u : 0u);
+              else
+                umma_ss(tbase + N * sb, desc_add(kdesc, (ks >> 2) * kBox + (ks & 3) * 32), qd, id, ks ? 1u : 0u);
+            }
             umma_commit(smem_u32(&sm.s_full[sb]));
+            umma_commit(smem_u32(&sm.kempty[n % KS]));
           }
           ++seg;
         }
       } else {
-        // A = the same tile read MN-major (two 64-column boxes an M block, LBO between them), B = P^T,
+        // A = the value tile read MN-major (two 64-column boxes an M block, LBO between them), B = P^T,
         // MN-major: 8-key atoms of 8 * 2N bytes, swizzled over the 2N bytes of a key's rows
         const uint32_t id = idesc_bf16(128, N, 1, 1);
         constexpr uint32_t atom = 16 * N;
@@ -483,14 +492,14 @@ __global__ void __launch_bounds__(PagedCfg<D, N>::kThreads, 1) paged_decode_kern
             const uint64_t pdesc = N == 64 ? sdesc_sw128(paddr, 16, atom) : N == 32 ? sdesc_sw64(paddr, 16, atom) : sdesc_sw32(paddr, 16, atom);
 #pragma unroll
             for (int mb = 0; mb < Cfg::kMB; ++mb) {
-              const uint64_t vdesc = sdesc_sw128(stage_base + (n % KS) * Cfg::kStage + 2 * mb * kBox, kBox, 1024);
+              const uint64_t vdesc = sdesc_sw128(v_base + (n % VS) * Cfg::kVStage + 2 * mb * kBox, kBox, 1024);
 #pragma unroll
               for (int kk = 0; kk < TN / 16; ++kk)
                 umma_ss(tbase + O0 + N * mb, desc_add(vdesc, kk * 2048), desc_add(pdesc, kk * 2 * atom), id,
                         first && kk == 0 ? 0u : 1u);
             }
             umma_commit(smem_u32(&sm.o_done[pb]));
-            umma_commit(smem_u32(&sm.empty[n % KS]));
+            umma_commit(smem_u32(&sm.vempty[n % VS]));
           }
           ++seg;
         }
@@ -503,38 +512,39 @@ __global__ void __launch_bounds__(PagedCfg<D, N>::kThreads, 1) paged_decode_kern
     }
   } else if (warp >= Cfg::kConv0) {
     // ================================================================== converters
-    // A group of kTileWarps takes every kTurns-th tile, warp w of it kWarpKeys keys of the tile.  A lane takes the rows lane % 8 + 8 k and, of each, the 32-column chunks lane / 8 + 4 h: eight lanes then write eight
-    // different 16-byte columns of the swizzled rows (no bank conflicts), and a warp's load covers whole sectors of
-    // eight rows.  A tile's rows are asked into L2 while the group converts the tile before it, and their page numbers
-    // one tile earlier still; while one group waits for its loads another converts.
-    constexpr int kKeys = Cfg::kWarpKeys, kK = kKeys / 8, kH = D / 128;
-    const int w = (warp - Cfg::kConv0) % Cfg::kTileWarps, rl = lane & 7, cl = lane >> 3;
+    // Warp w takes 16 keys of every tile: lanes 16 (w / 4) .. + 15 of the TMEM quadrant w % 4, the keys g and g + 8 in
+    // thread 4g + c, and of each key the 32-column chunks c + 4h and the 16-byte pieces c and c + 4 of its RoPE key, so
+    // that a warp's load covers 64 contiguous bytes of eight rows.  tcgen05.st 16x128b puts register 2j (2j + 1) of
+    // that thread at key g (g + 8), column 4j + c: the K index of QK runs through the columns in that order, and Q is
+    // stored to match.  Chunks with c & 2 are expanded second half first: eight lanes then write eight different
+    // 16-byte columns of the value tile (no bank conflicts).  The next tile's loads are issued when this one is
+    // converted; its rows were asked into L2 a tile earlier, and their page numbers one tile earlier still.
+    constexpr int kKeys = kPagedTile / kPagedConv, kH = D / 128;
+    const int cw = warp - Cfg::kConv0, key0 = 32 * (cw & 3) + 16 * (cw >> 2);
+    const int g = lane >> 2, c = lane & 3;
     const int r = p.G * D;
     const uint8_t* pool = p.pages.pool;
     const int key_at = int4_rope_at(r);
     struct Tile {
       int b, t, L, group;  // t < 0: none
     };
-    PagedCursor& walk = sm.walk[SW + warp - Cfg::kConv0];
-    PagedSegment& seg = sm.conv_seg[warp - Cfg::kConv0];
+    PagedCursor& walk = sm.walk[SW + cw];
+    PagedSegment& seg = sm.conv_seg[cw];
     if (lane == 0) walk = sm.cur;
     int walk_t = 0, walk_hi = 0;
-    auto next_tile = [&](int skip) -> Tile {
-      for (;; --skip) {
-        if (walk_t >= walk_hi) {
-          if (!paged_next(p, N, walk, seg, lane)) return Tile{0, -1, 0, 0};
-          walk_t = seg.tile_lo;
-          walk_hi = seg.tile_hi;
-        }
-        if (skip == 0) return Tile{seg.b, walk_t++, seg.L, seg.group};
-        ++walk_t;
+    auto next_tile = [&]() -> Tile {
+      if (walk_t >= walk_hi) {
+        if (!paged_next(p, N, walk, seg, lane)) return Tile{0, -1, 0, 0};
+        walk_t = seg.tile_lo;
+        walk_hi = seg.tile_hi;
       }
+      return Tile{seg.b, walk_t++, seg.L, seg.group};
     };
     // this lane's key of a tile: the page is asked for here, used a tile later
     int page = -1, slot = 0;
     bool key_live = false;
     auto ask_page = [&](const Tile& x) {
-      const int key = x.t * TN + kKeys * w + lane;
+      const int key = x.t * TN + key0 + lane;
       key_live = x.t >= 0 && lane < kKeys && key < x.L;
       page = -1;
       if (key_live) {
@@ -556,25 +566,24 @@ __global__ void __launch_bounds__(PagedCfg<D, N>::kThreads, 1) paged_decode_kern
       prefetch_l2(row + key_at);
       return off;
     };
-    uint4 code[kK][kH], key[kK][2];
-    uint32_t scale[kK][kH];
+    uint4 code[2][kH], key[2][2];
+    uint32_t scale[2][kH];
     auto load_rows = [&](long long off, int group) {
-      const uint8_t* cp = pool + 16 * cl + group * (D / 2);
-      const uint8_t* sp = pool + 2 * cl + r / 2 + group * (D / 16);
-      const uint8_t* kp = pool + 16 * cl + key_at;
-      auto row = [&](int k) { return __shfl_sync(0xffffffffu, off, 8 * k + rl); };
+      const uint8_t* cp = pool + 16 * c + group * (D / 2);
+      const uint8_t* sp = pool + 2 * c + r / 2 + group * (D / 16);
+      const uint8_t* kp = pool + 16 * c + key_at;
       if (__all_sync(0xffffffffu, off >= 0 || lane >= kKeys)) {
 #pragma unroll
-        for (int k = 0; k < kK; ++k) {
-          const long long at = row(k);
+        for (int k = 0; k < 2; ++k) {
+          const long long at = __shfl_sync(0xffffffffu, off, 8 * k + g);
           static_for<kH>([&](auto h) { code[k][h] = ldg16<64 * h>(cp + at); });
           static_for<kH>([&](auto h) { scale[k][h] = ldg2<8 * h>(sp + at); });
           static_for<2>([&](auto h) { key[k][h] = ldg16<64 * h>(kp + at); });
         }
       } else {  // rows without a token: codes 0 times scale 0, and a key of zeros
 #pragma unroll
-        for (int k = 0; k < kK; ++k) {
-          const long long at = row(k);
+        for (int k = 0; k < 2; ++k) {
+          const long long at = __shfl_sync(0xffffffffu, off, 8 * k + g);
           static_for<kH>([&](auto h) { code[k][h] = ldg16_if<64 * h>(cp + at, at >= 0); });
           static_for<kH>([&](auto h) { scale[k][h] = ldg2_if<8 * h>(sp + at, at >= 0); });
           static_for<2>([&](auto h) { key[k][h] = ldg16_if<64 * h>(kp + at, at >= 0); });
@@ -583,46 +592,76 @@ __global__ void __launch_bounds__(PagedCfg<D, N>::kThreads, 1) paged_decode_kern
     };
     uint32_t mask = 0x000f000fu, magic = 0x43004300u;
     asm volatile("" : "+r"(mask), "+r"(magic));
-    // where this lane's 16-byte pieces of a row go: word e of a chunk, and the RoPE key's two
-    uint32_t at_code[4], at_key[2];
+    // where word e of this lane's chunk goes in the value tile (key g + 8: 1024 bytes on)
+    uint32_t at_word[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) at_code[e] = (kKeys * w + rl) * 128 + (cl >> 1) * kBox + (((4 * (cl & 1) + e) ^ rl) << 4);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) at_key[h] = (kKeys * w + rl) * 128 + Cfg::kKBoxes * kBox + (((cl + 4 * h) ^ rl) << 4);
-    int n = (warp - Cfg::kConv0) / Cfg::kTileWarps;
-    Tile now = next_tile(n), then = Tile{0, -1, 0, 0};
+    for (int e = 0; e < 4; ++e) at_word[e] = (key0 + g) * 128 + (c >> 1) * kBox + (((4 * (c & 1) + (e ^ (c & 2))) ^ g) << 4);
+    const uint32_t tlane = tbase + K0 + (static_cast<uint32_t>(key0) << 16);
+    Tile now = next_tile(), then = Tile{0, -1, 0, 0};
     ask_page(now);
-    long long off = row_of_page(now);
-    if (now.t >= 0) then = next_tile(Cfg::kTurns - 1);
-    ask_page(then);
-    for (; now.t >= 0; n += Cfg::kTurns) {
+    long long off = row_of_page(now), off_then = -1;
+    if (now.t >= 0) {
       load_rows(off, now.group);
-      const long long off_then = row_of_page(then);
-      const Tile later = then.t >= 0 ? next_tile(Cfg::kTurns - 1) : then;
-      ask_page(later);
-      const int st = n % KS;
-      if (n >= KS && !wait_all(sm.empty[st], n / KS - 1, PW_EMPTY)) break;
-      uint8_t* stage = dsm + st * Cfg::kStage;
+      then = next_tile();
+    }
+    ask_page(then);
+    if (then.t >= 0) off_then = row_of_page(then);
+    Tile later = then.t >= 0 ? next_tile() : then;
+    ask_page(later);
+    for (int n = 0; now.t >= 0; ++n) {
+      if ((n >= KS && !wait_all(sm.kempty[n % KS], n / KS - 1, PW_KEMPTY)) ||
+          (n >= VS && !wait_all(sm.vempty[n % VS], n / VS - 1, PW_VEMPTY)))
+        break;
+      uint8_t* stage = dsm + (n % VS) * Cfg::kVStage;
+      const uint32_t ktm = tlane + (n % KS) * Cfg::kKCols;
+      tc_fence_after();
 #pragma unroll
-      for (int k = 0; k < kK; ++k) {
+      for (int h = 0; h < kH; ++h) {
+        uint32_t out[32];
 #pragma unroll
-        for (int h = 0; h < kH; ++h) {
+        for (int k = 0; k < 2; ++k) {
           const uint32_t s2 = __byte_perm(scale[k][h], 0, 0x1010);
           const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&s2);
           const __nv_bfloat162 o = __hmul2(s, __float2bfloat162_rn(-136.f));
-          const uint32_t word[4] = {code[k][h].x, code[k][h].y, code[k][h].z, code[k][h].w};
+          const uint4 v = code[k][h];
+          const bool swap = (c & 2) != 0;
+          const uint32_t word[4] = {swap ? v.z : v.x, swap ? v.w : v.y, swap ? v.x : v.z, swap ? v.y : v.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<uint4*>(stage + at_code[e] + 2 * h * kBox + 1024 * k) = int4_expand(word[e], mask, magic, s, o);
+          for (int e = 0; e < 4; ++e) {
+            const uint4 x = int4_expand(word[e], mask, magic, s, o);
+            *reinterpret_cast<uint4*>(stage + at_word[e] + 2 * h * kBox + 1024 * k) = x;
+            out[8 * e + k] = x.x;
+            out[8 * e + 2 + k] = x.y;
+            out[8 * e + 4 + k] = x.z;
+            out[8 * e + 6 + k] = x.w;
+          }
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) *reinterpret_cast<uint4*>(stage + at_key[h] + 1024 * k) = key[k][h];
+        if (Cfg::kTS) tmem_st_16x128_x16(ktm + 64 * h, out);
       }
+      {
+        uint32_t out[16];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            out[8 * h + k] = key[k][h].x;
+            out[8 * h + 2 + k] = key[k][h].y;
+            out[8 * h + 4 + k] = key[k][h].z;
+            out[8 * h + 6 + k] = key[k][h].w;
+          }
+        }
+        tmem_st_16x128_x8(ktm + (Cfg::kTS ? D / 2 : 0), out);
+      }
+      if (then.t >= 0) load_rows(off_then, then.group);
+      tmem_wait_st();
       fence_proxy_async_smem();
-      warp_arrive(sm.full[st]);
+      tc_fence_before();
+      warp_arrive(sm.full[n % VS]);
       now = then;
       then = later;
-      off = off_then;
+      off_then = row_of_page(then);
+      if (then.t >= 0) later = next_tile();
+      ask_page(later);
     }
   } else if (warp >= 4) {
     // ================================================================== softmax / epilogue
@@ -674,26 +713,30 @@ __global__ void __launch_bounds__(PagedCfg<D, N>::kThreads, 1) paged_decode_kern
       const int lim0 = sg.L - p.s_q;               // query i sees keys 0 .. lim0 + i
       const int newest = p.hpg - (sg.row0 + rb);   // rows from here on are query 1's (or padding)
       for (int t = t_lo; t < t_hi; ++t, ++n) {
-        const int sb = n & 1, pb = n % PS;
+        const int sb = n % SS, pb = n % PS;
         const bool first = t == t_lo;
-        if (!wait_all(sm.s_full[sb], n >> 1, PW_SFULL)) {
+        if (!wait_all(sm.s_full[sb], n / SS, PW_SFULL)) {
           ok = false;
           break;
         }
         tc_fence_after();
         // the tile's scores, -inf where the row does not see the key
         float x[RW];
-        auto load_scores = [&] {
-          tmem_load_rows<RW>(tlane + N * sb + rb, x);
-          tmem_wait_ld();
-          if ((t + 1) * TN - 1 > lim0) {
-            const int ahead = t * TN + k - lim0;
+        tmem_load_rows<RW>(tlane + N * sb + rb, x);
+        tmem_wait_ld();
+        tc_fence_before();
+        warp_arrive(sm.s_free[sb]);
+        if ((t + 1) * TN - 1 > lim0) {
+          const int ahead = t * TN + k - lim0;
 #pragma unroll
-            for (int j = 0; j < RW; ++j)
-              if (ahead > (j >= newest ? 1 : 0)) x[j] = -INFINITY;
-          }
-        };
-        auto sub_reference = [&]() -> float {
+          for (int j = 0; j < RW; ++j)
+            if (ahead > (j >= newest ? 1 : 0)) x[j] = -INFINITY;
+        }
+        bool raise = first;
+        if (first) {
+#pragma unroll
+          for (int j = 0; j < RW; ++j) x[j] *= p.sl2;
+        } else {
           float top = -INFINITY;
 #pragma unroll
           for (int j4 = 0; j4 < RW / 4; ++j4) {
@@ -704,36 +747,6 @@ __global__ void __launch_bounds__(PagedCfg<D, N>::kThreads, 1) paged_decode_kern
             x[4 * j4 + 3] = fmaf(x[4 * j4 + 3], p.sl2, -r4.w);
             top = fmaxf(top, fmaxf(fmaxf(x[4 * j4], x[4 * j4 + 1]), fmaxf(x[4 * j4 + 2], x[4 * j4 + 3])));
           }
-          return top;
-        };
-        // Take the scores against the references and vote; where there is none yet, or the vote asks for it, find the
-        // tile's maxima, raise the references and take the scores again (a second reading spares a copy of them).
-        enum { kVote, kFind, kTake };
-        int step = first ? kFind : kVote;
-        while (true) {
-          if (step == kFind) {
-            const float mw = paged_find_max<RW>(tlane + N * sb + rb, t * TN + k - lim0, newest, lane);
-            float all[4];
-            if (!exchange(mw, all)) {
-              ok = false;
-              break;
-            }
-            const float mt = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3])) * p.sl2;
-            // a row that sees no key of the segment's first tile sees none of its later ones
-            const float m_new = first ? (mt == -INFINITY ? 0.f : mt) : fmaxf(m_run, mt);
-            if (lane < RW) {
-              sm.ref[sw][lane] = m_new;
-              sm.fac[sw][lane] = first ? 0.f : ex2_approx(m_run - m_new);
-            }
-            m_run = m_new;
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < RW; ++j) l[j] = first ? 0.f : l[j] * sm.fac[sw][j];
-            step = kTake;
-          }
-          load_scores();
-          const float top = sub_reference();
-          if (step == kTake) break;
           // The flag of vote vc is one of three words: it is cleared after vote vc + 1, when every warp has read
           // it, and set again for vote vc + 3 by warps that passed vote vc + 2, which this warp joins after clearing.
           if (__any_sync(0xffffffffu, top > kPagedRaise) && lane == 0) *const_cast<volatile uint32_t*>(&sm.vote[vc % 3]) = 1u;
@@ -742,15 +755,39 @@ __global__ void __launch_bounds__(PagedCfg<D, N>::kThreads, 1) paged_decode_kern
             ok = false;
             break;
           }
-          const bool raise = *const_cast<volatile uint32_t*>(&sm.vote[vc % 3]) != 0;  // the same for all softmax warps
+          raise = *const_cast<volatile uint32_t*>(&sm.vote[vc % 3]) != 0;  // the same for all softmax warps
           if (sw == 0 && lane == 0) *const_cast<volatile uint32_t*>(&sm.vote[(vc + 2) % 3]) = 0u;
           ++vc;
-          if (!raise) break;
-          step = kFind;
         }
-        if (!ok) break;
-        tc_fence_before();
-        warp_arrive(sm.s_free[sb]);
+        if (raise) {
+          // the rows' maxima over the tile's keys, above the references (the first tile's references are 0)
+          float mw = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < RW; ++j) {
+            const float v = warp_max(x[j]);
+            if (rl == j) mw = v;
+          }
+          float all[4];
+          if (!exchange(mw, all)) {
+            ok = false;
+            break;
+          }
+          const float mt = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
+          // a row that sees no key of the segment's first tile sees none of its later ones: its reference stays 0
+          const float up = first ? (mt == -INFINITY ? 0.f : mt) : fmaxf(mt, 0.f);
+          m_run = first ? up : m_run + up;
+          if (lane < RW) {
+            sm.ref[sw][lane] = m_run;
+            sm.fac[sw][lane] = up;
+          }
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < RW; ++j) {
+            const float u = *const_cast<volatile float*>(&sm.fac[sw][j]);
+            x[j] -= u;
+            l[j] = first ? 0.f : l[j] * ex2_approx(-u);
+          }
+        }
         if (t == t_hi - 1 && (have_nx = paged_next(p, N, walk, nx, lane))) load_q(nx);  // this unit's QKs are done
         uint32_t pw[RW / 2];
 #pragma unroll
@@ -775,7 +812,7 @@ __global__ void __launch_bounds__(PagedCfg<D, N>::kThreads, 1) paged_decode_kern
                 make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
         }
         fence_proxy_async_smem();
-        if (step == kTake && !first) {
+        if (raise && !first) {
           // O^T holds the segment's tiles up to n - 1
           if (!wait_all(sm.o_done[(n - 1) % PS], (n - 1) / PS, PW_ODONE)) {
             ok = false;
