@@ -67,9 +67,8 @@ void launch_rope(const RopeParams& p, bool interleaved, unsigned blocks, cudaStr
 }
 
 // Rows of a unit (the MMA's N): the smallest of 16, 32, 64 that holds a group's rows, so that small groups
-// spend no softmax on padding; 64 at most (32 where 512 columns of Q and of a tile fill shared memory), and
-// a group of more rows is several units that read the same tiles.
-int paged_rows(int R, int d) { return R <= 16 ? 16 : R <= 32 || d == 512 ? 32 : 64; }
+// spend no softmax on padding; 64 at most, and a group of more rows is several units that read the same tiles.
+int paged_rows(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }
 
 struct PagedPlan {
   int N, RB, U, P, lockstep;
@@ -78,7 +77,7 @@ struct PagedPlan {
 
 void paged_plan(PagedPlan* w, int s_q, int h_q, int groups, int d, int num_sms) {
   const int R = s_q * (h_q / groups);
-  w->N = paged_rows(R, d);
+  w->N = paged_rows(R);
   w->RB = (R + w->N - 1) / w->N;
   w->U = groups * w->RB;
   // Units in lockstep share a request's RoPE keys and scales through L2; not where that leaves more than a
@@ -111,7 +110,7 @@ lkv_status launch_decode(const PagedDecodeParams& p, cudaStream_t s) {
     }
     ready[dev] = true;
   }
-  paged_decode_kernel<D, N><<<p.P, Cfg::kThreads, Cfg::kSmem, s>>>(p);
+  paged_decode_kernel<D, N><<<p.P, kPagedThreads, Cfg::kSmem, s>>>(p);
   const lkv_status st = launched();
   if (st != LKV_OK) return st;
   cudaLaunchConfig_t cfg = {};
@@ -131,7 +130,7 @@ lkv_status launch_decode(const PagedDecodeParams& p, cudaStream_t s) {
 lkv_status launch_decode_for(const PagedDecodeParams& p, int d, int N, cudaStream_t s) {
   if (d == 128) return N == 16 ? launch_decode<128, 16>(p, s) : N == 32 ? launch_decode<128, 32>(p, s) : launch_decode<128, 64>(p, s);
   if (d == 256) return N == 16 ? launch_decode<256, 16>(p, s) : N == 32 ? launch_decode<256, 32>(p, s) : launch_decode<256, 64>(p, s);
-  return N == 16 ? launch_decode<512, 16>(p, s) : launch_decode<512, 32>(p, s);
+  return N == 16 ? launch_decode<512, 16>(p, s) : N == 32 ? launch_decode<512, 32>(p, s) : launch_decode<512, 64>(p, s);
 }
 
 }  // namespace

@@ -30,7 +30,8 @@
 
 namespace lkv {
 
-constexpr int kPagedConv = 8;  // converter warps
+constexpr int kPagedConv = 8;                          // converter warps
+constexpr int kPagedThreads = 32 * (4 + 8 + kPagedConv);  // issuers, softmax, converters
 constexpr int kPagedTile = 128;
 constexpr float kPagedRaise = 64.f;  // log2 units a score may pass its row's reference by
 
@@ -158,46 +159,39 @@ struct PagedCfg {
   // A there, 32 cycles of its bandwidth; from TMEM it runs at the tensor core's rate, 16 cycles at N = 32), else from
   // the value operand's tile; the RoPE key from TMEM always.
   static constexpr bool kTS = D <= 256;
-  static constexpr int kKCols = (kTS ? D / 2 : 0) + 32;  // TMEM columns of a key stage
-  static constexpr int kVStages = D == 128 ? 3 : D == 256 ? 2 : 1;
-  static constexpr int kKStages = D == 128 ? 3 : 2;
+  static constexpr int kKCols = (kTS ? D / 2 : 0) + 32;  // TMEM columns of a stage: the key operand
+  static constexpr int kStages = D == 128 ? 3 : D == 256 ? 2 : 1;
+  static constexpr int kRW = N / 2;  // rows of a softmax warp: two sets of four warps, one warp for each TMEM lane quadrant
   static constexpr int kSBufs = D == 256 && N == 64 ? 1 : 2;  // S^T buffers
   static constexpr int kPs = D == 512 && N == 64 ? 1 : 2;     // P buffers
   static constexpr int kQBox = N * 128;
   static constexpr int kQBytes = (kVBoxes + 1) * kQBox;
   static constexpr int kPBytes = kPagedTile * N * 2;
-  // Softmax warps: four, one for each TMEM lane quadrant, with all N rows (a warp's waits and arrivals cost about as
-  // much as 16 rows do); 64 rows are split between two such sets, for their registers.
-  static constexpr int kSW = N == 64 ? 8 : 4;
-  static constexpr int kRW = 4 * N / kSW;   // rows of a softmax warp
-  static constexpr int kConv0 = 4 + kSW;    // first converter warp
-  static constexpr int kThreads = 32 * (kConv0 + kPagedConv);
-  static constexpr int kMB = D / 128;       // M blocks of PV
-  static constexpr uint32_t kO0 = kSBufs * N, kK0 = kO0 + kMB * N;  // TMEM: S^T buffers, O^T, key stages
-  static constexpr int kTmemNeed = kK0 + kKStages * kKCols;
+  static constexpr int kMB = D / 128;            // M blocks of PV
+  static constexpr uint32_t kO0 = kSBufs * N, kK0 = (kO0 + kMB * N + 31) / 32 * 32;  // TMEM: S^T buffers, O^T, key stages
+  static constexpr int kTmemNeed = kK0 + kStages * kKCols;
   static constexpr int kTmemCols = kTmemNeed <= 128 ? 128 : kTmemNeed <= 256 ? 256 : 512;
-  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kVStages) * kVStage + kQBytes + kPs * kPBytes;
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kVStage + kQBytes + kPs * kPBytes;
   static_assert(kTmemNeed <= 512, "TMEM budget");
   static_assert(kSmem <= 232448 - 8192, "shared memory budget");
 };
 
 constexpr int kPagedSite = LKV_SITE_WAIT_BASE + 300;  // wait sites of this kernel
-enum PagedWaitSite { PW_KEMPTY = 1, PW_VEMPTY, PW_FULL, PW_SFREE, PW_QREADY, PW_PFULL, PW_OFREE, PW_SFULL, PW_ODONE, PW_VOTE, PW_XCHG, PW_DRAIN };
+enum PagedWaitSite { PW_EMPTY = 1, PW_FULL, PW_SFREE, PW_QREADY, PW_PFULL, PW_OFREE, PW_SFULL, PW_ODONE, PW_VOTE, PW_XCHG, PW_DRAIN };
 
-template <int RW, int SW>
+template <int RW>
 struct __align__(16) PagedSmem {
-  uint64_t full[3], kempty[3], vempty[3];
+  uint64_t full[3], empty[3];
   uint64_t s_full[2], s_free[2], p_full[2], o_done[2];
-  uint64_t q_ready, o_free, drain, vote_bar, xchg_bar;
-  alignas(16) float red[2][SW][RW];  // [buffer][softmax warp][its row]
-  alignas(16) float ref[SW][RW];     // per warp: its rows' references (log2 units)
-  alignas(16) float fac[SW][RW];     // per warp: what the references rose by, then 1 / l
+  uint64_t q_ready, o_free, vote_bar, xchg_bar, drain;
+  alignas(16) float red[2][8][RW];    // [buffer][softmax warp][its row]
+  alignas(16) float ref[8][RW];       // per softmax warp: its rows' references (log2 units)
+  alignas(16) float fac[8][RW];       // per softmax warp: what the references rose by, then 1 / l
   uint32_t vote[3];
   uint32_t tmem_base, abort;
-  PagedCursor cur;
   // Walk state of the warps that run out of registers first: read where it is needed.
-  PagedCursor walk[SW + kPagedConv];
-  PagedSegment seg[SW][2], conv_seg[kPagedConv];
+  PagedCursor cur, walk[8 + kPagedConv];
+  PagedSegment seg[8][2], conv_seg[kPagedConv];
 };
 
 // The next segment of a warp's own walk, both in shared memory; the same answer in every lane.
@@ -206,6 +200,28 @@ __device__ __noinline__ bool paged_next(const PagedDecodeParams& p, int rows, Pa
   __syncwarp();
   if (lane == 0) ok = walk.next(p, rows, out);
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+// The wait on a phase that one test did not find complete.  It gives up after a limit, records the site and sets the
+// block's abort flag; every later wait of the block then returns at once and its work runs on garbage, in bounds, to
+// its end, which keeps a test of each wait's outcome out of the loops.
+__device__ __noinline__ void paged_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t* abort, int* err, uint64_t limit_ns, int site) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t it = 1; !mbar_sleep_test(bar, parity); ++it) {
+    if (*abort) return;
+    if ((it & 15u) == 0 && globaltimer_ns() - t0 > limit_ns) {
+      record_error(err, site);
+      *abort = 1u;
+    }
+  }
+}
+
+// Key k's row in the value tile and in P^T: bits 1, 2, 3 of k move to 2, 3, 1.  The lanes that expand keys g and g + 8
+// then write different 16-byte columns of the swizzled rows.  (Where the value tile is the key operand too, its rows are
+// the lanes of S^T, and stay.)
+template <bool kTS>
+__device__ __forceinline__ int paged_key_row(int k) {
+  return kTS ? (k & ~14) | ((k >> 2) & 2) | ((k & 6) << 1) : k;
 }
 
 template <int RW>
@@ -254,26 +270,17 @@ __device__ __forceinline__ float paged_rows_reduce(float (&v)[RW], int lane) {
 }
 
 // Loads at a constant offset.  Volatile: the compiler keeps them where they are, ahead of the waits that their
-// latency is to overlap.  The _if forms give zeros where `ok` is 0.
+// latency is to overlap.
 template <int kAt>
 __device__ __forceinline__ uint4 ldg16(const uint8_t* ptr) {
   uint4 v;
   asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4+%5];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(ptr), "n"(kAt));
   return v;
 }
-template <int kAt>
-__device__ __forceinline__ uint32_t ldg2(const uint8_t* ptr) {
-  uint32_t v;
-  asm volatile("{\n\t.reg .u16 h;\n\tld.global.nc.u16 h, [%1+%2];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(v) : "l"(ptr), "n"(kAt));
+__device__ __forceinline__ uint2 ldg8(const uint8_t* ptr) {
+  uint2 v;
+  asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(ptr));
   return v;
-}
-template <int kAt>
-__device__ __forceinline__ uint4 ldg16_if(const uint8_t* ptr, bool ok) {
-  return ok ? ldg16<kAt>(ptr) : make_uint4(0u, 0u, 0u, 0u);
-}
-template <int kAt>
-__device__ __forceinline__ uint32_t ldg2_if(const uint8_t* ptr, bool ok) {
-  return ok ? ldg2<kAt>(ptr) : 0u;
 }
 __device__ __forceinline__ void prefetch_l2(const uint8_t* ptr) { asm volatile("prefetch.global.L2 [%0];" ::"l"(ptr)); }
 
@@ -304,14 +311,14 @@ __device__ __forceinline__ uint4 int4_expand(uint32_t w, uint32_t mask, uint32_t
 // The softmax warps' rare work, out of line: inlined, its registers spilled the loop's over every tile (a spill's
 // reload misses an L1 that streams codes, and cost the loop more than half of its time).
 // ------------------------------------------------------------------------------------------
-// A segment's Q as the K-major B operand, rows behind the group's last as zeros.  16-byte piece j of what the
-// converters put into TMEM holds the column pairs of the four lanes c = 0 .. 3: of a 128-column block, with j = 4e + i,
-// columns 32c + 8 (e ^ (c & 2)) + 2i; of the RoPE key 8c + 2j for j < 4, then 32 + 8c + 2 (j - 4).
-template <int D, int N, int kThreads>
-__device__ __noinline__ void paged_load_q(const PagedDecodeParams& p, const PagedSegment& s, uint8_t* qsm, int first) {
+// A segment's Q as the K-major B operand, rows behind the group's last as zeros.  The columns follow what the converters
+// put into TMEM: register j of half h of a 128-column block is columns 32 (h + 2m) + 8e + 2i with j = 16m + 4e + i, of the
+// RoPE key 8 (h + 2m) + 2i with j = 4m + i, and a 16-byte piece p holds j = 2p and 2p + 1, each for h = 0 and 1.
+template <int D, int N>
+__device__ __noinline__ void paged_load_q(const PagedDecodeParams& p, const PagedSegment& s, uint8_t* qsm, int first, int step) {
   constexpr int kC = (D + 64) / 8;
 #pragma unroll 2
-  for (int idx = first; idx < N * kC; idx += kThreads) {
+  for (int idx = first; idx < N * kC; idx += step) {
     const int row = idx / kC, piece = idx % kC;
     const int bx = piece >> 3, cc = piece & 7, g = s.row0 + row;
     uint4 x = make_uint4(0u, 0u, 0u, 0u);
@@ -320,12 +327,12 @@ __device__ __noinline__ void paged_load_q(const PagedDecodeParams& p, const Page
       const size_t qrow = (static_cast<size_t>(s.b) * p.s_q + i) * p.h_q + s.group * p.hpg + (g - i * p.hpg);
       const __nv_bfloat16* q = p.q + qrow * D;
       if (piece >= D / 8) {
-        const uint32_t* k = reinterpret_cast<const uint32_t*>(p.q_rope + qrow * 64) + (cc < 4 ? cc : 12 + cc);
-        x = make_uint4(__ldg(k), __ldg(k + 4), __ldg(k + 8), __ldg(k + 12));
+        const uint32_t* k = reinterpret_cast<const uint32_t*>(p.q_rope + qrow * 64) + 8 * (cc >> 1) + 2 * (cc & 1);
+        x = make_uint4(__ldg(k), __ldg(k + 4), __ldg(k + 1), __ldg(k + 5));
       } else if (PagedCfg<D, N>::kTS) {
-        const int j = piece & 15, e = j >> 2;
-        const uint32_t* k = reinterpret_cast<const uint32_t*>(q) + 64 * (piece >> 4) + (j & 3);
-        x = make_uint4(__ldg(k + 4 * e), __ldg(k + 16 + 4 * e), __ldg(k + 32 + 4 * (e ^ 2)), __ldg(k + 48 + 4 * (e ^ 2)));
+        const int j = piece & 15;
+        const uint32_t* k = reinterpret_cast<const uint32_t*>(q) + 64 * (piece >> 4) + 32 * (j >> 3) + 4 * ((j >> 1) & 3) + 2 * (j & 1);
+        x = make_uint4(__ldg(k), __ldg(k + 16), __ldg(k + 1), __ldg(k + 17));
       } else {
         x = __ldg(reinterpret_cast<const uint4*>(q) + piece);
       }
@@ -350,17 +357,17 @@ __device__ __noinline__ void paged_rescale(uint32_t tmem, const float* up) {
   tmem_wait_st();
 }
 
-// O^T times 1 / l: the result, or the range's partial.  c: this thread's value column of each M block.
-template <int D, int N, int RW, int kMB>
+// O^T times 1 / l: the result, or the range's partial.  c: this thread's value column of an M block.
+template <int D, int N, int RW>
 __device__ __noinline__ void paged_store_out(const PagedDecodeParams& p, const PagedSegment& s, uint32_t tmem, const float* inv, int rb,
                                              int c, size_t part) {
   const int n = min(RW, p.R - (s.row0 + rb));
+  const size_t row0 = static_cast<size_t>(s.b) * p.s_q * p.h_q + s.group * p.hpg;
 #pragma unroll 1
-  for (int mb = 0; mb < kMB; ++mb, c += 128) {
+  for (int mb = 0; mb < D / 128; ++mb, c += 128) {
     float o[RW];
     tmem_load_rows<RW>(tmem + N * mb, o);
     tmem_wait_ld();
-    const size_t row0 = static_cast<size_t>(s.b) * p.s_q * p.h_q + s.group * p.hpg;
 #pragma unroll
     for (int j = 0; j < RW; ++j) {
       if (j >= n) break;
@@ -375,18 +382,17 @@ __device__ __noinline__ void paged_store_out(const PagedDecodeParams& p, const P
 }
 
 template <int D, int N>
-__global__ void __launch_bounds__(PagedCfg<D, N>::kThreads, 1) paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
+__global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
   using Cfg = PagedCfg<D, N>;
-  constexpr int TN = kPagedTile, VS = Cfg::kVStages, KS = Cfg::kKStages, SS = Cfg::kSBufs, PS = Cfg::kPs;
-  constexpr int RW = Cfg::kRW, SW = Cfg::kSW;
+  constexpr int TN = kPagedTile, ST = Cfg::kStages, SS = Cfg::kSBufs, PS = Cfg::kPs;
+  constexpr int RW = Cfg::kRW, MB = Cfg::kMB;
   constexpr int kBox = Cfg::kBox;
   constexpr uint32_t O0 = Cfg::kO0, K0 = Cfg::kK0;
-  constexpr int SB = kPagedSite;
 
   extern __shared__ __align__(1024) uint8_t paged_smem_raw[];
-  __shared__ PagedSmem<RW, SW> sm;
+  __shared__ PagedSmem<RW> sm;
   uint8_t* dsm = paged_smem_raw + ((1024u - (smem_u32(paged_smem_raw) & 1023u)) & 1023u);
-  uint8_t* qsm = dsm + VS * Cfg::kVStage;
+  uint8_t* qsm = dsm + ST * Cfg::kVStage;
   uint8_t* psm = qsm + Cfg::kQBytes;
   const uint32_t v_base = smem_u32(dsm), q_base = smem_u32(qsm), p_base = smem_u32(psm);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -395,20 +401,19 @@ __global__ void __launch_bounds__(PagedCfg<D, N>::kThreads, 1) paged_decode_kern
   if (tid == 0) {
     for (int s = 0; s < 3; ++s) {
       mbar_init(smem_u32(&sm.full[s]), kPagedConv);
-      mbar_init(smem_u32(&sm.kempty[s]), 1);
-      mbar_init(smem_u32(&sm.vempty[s]), 1);
+      mbar_init(smem_u32(&sm.empty[s]), 1);
       sm.vote[s] = 0;
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&sm.s_full[b]), 1);
-      mbar_init(smem_u32(&sm.s_free[b]), SW);  // the softmax warps
-      mbar_init(smem_u32(&sm.p_full[b]), SW);
+      mbar_init(smem_u32(&sm.s_free[b]), 8);  // the softmax warps
+      mbar_init(smem_u32(&sm.p_full[b]), 8);
       mbar_init(smem_u32(&sm.o_done[b]), 1);
     }
-    mbar_init(smem_u32(&sm.q_ready), SW);
-    mbar_init(smem_u32(&sm.o_free), SW);
-    mbar_init(smem_u32(&sm.vote_bar), SW);
-    mbar_init(smem_u32(&sm.xchg_bar), SW);
+    mbar_init(smem_u32(&sm.q_ready), 8);
+    mbar_init(smem_u32(&sm.o_free), 8);
+    mbar_init(smem_u32(&sm.vote_bar), 8);
+    mbar_init(smem_u32(&sm.xchg_bar), 8);
     mbar_init(smem_u32(&sm.drain), 2);  // one commit from each issuer
     sm.abort = 0;
     p.seg_info[2 * range] = -1;
@@ -428,9 +433,9 @@ __global__ void __launch_bounds__(PagedCfg<D, N>::kThreads, 1) paged_decode_kern
   tc_fence_after();
   if (tid == 0) griddep_launch_dependents();  // the combine may start launching
   const uint32_t tbase = sm.tmem_base;
-  const WaitCtl wc{&sm.abort, p.err, p.wait_limit_ns};
-  auto wait_all = [&](uint64_t& bar, int phase, int site) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), static_cast<uint32_t>(phase & 1), wc, SB + site)) != 0;
+  auto wait = [&](uint64_t& bar, int phase, int site) {
+    const uint32_t a = smem_u32(&bar), par = static_cast<uint32_t>(phase & 1);
+    if (!mbar_test(a, par)) paged_wait_slow(a, par, &sm.abort, p.err, p.wait_limit_ns, kPagedSite + site);
   };
   auto warp_arrive = [&](uint64_t& bar) {
     __syncwarp();
@@ -443,23 +448,21 @@ __global__ void __launch_bounds__(PagedCfg<D, N>::kThreads, 1) paged_decode_kern
       PagedCursor cur = sm.cur;
       PagedSegment sg;
       int n = 0, seg = 0;
-      bool ok = true;
+      auto aborted = [&] { return *const_cast<volatile uint32_t*>(&sm.abort) != 0; };
       if (warp == 0) {
         // A = the key tile (state and RoPE key in TMEM; for D = 512 the state in shared memory), B = Q, K-major
         const uint32_t id = idesc_bf16(128, N, 0, 0);
         const uint64_t qdesc = sdesc_sw128(q_base, 16, 1024);
-        while (ok && cur.next(p, N, sg)) {
+        for (; cur.next(p, N, sg) && !aborted(); ++seg) {
           for (int t = sg.tile_lo; t < sg.tile_hi; ++t, ++n) {
-            const int sb = n % SS;
-            if (!mbar_wait(smem_u32(&sm.full[n % VS]), static_cast<uint32_t>((n / VS) & 1), wc, SB + PW_FULL) ||
-                (n >= SS && !mbar_wait(smem_u32(&sm.s_free[sb]), static_cast<uint32_t>((n / SS - 1) & 1), wc, SB + PW_SFREE)) ||
-                (t == sg.tile_lo && !mbar_wait(smem_u32(&sm.q_ready), static_cast<uint32_t>(seg & 1), wc, SB + PW_QREADY))) {
-              ok = false;
-              break;
-            }
+            const int sb = n % SS, st = n % ST;
+            wait(sm.full[st], n / ST, PW_FULL);
+            if (n >= SS) wait(sm.s_free[sb], n / SS - 1, PW_SFREE);
+            if (t == sg.tile_lo) wait(sm.q_ready, seg, PW_QREADY);
+            if (aborted()) break;
             tc_fence_after();
-            const uint32_t ktm = tbase + K0 + (n % KS) * Cfg::kKCols;
-            const uint64_t kdesc = sdesc_sw128(v_base + (n % VS) * Cfg::kVStage, 16, 1024);
+            const uint32_t ktm = tbase + K0 + st * Cfg::kKCols;
+            const uint64_t kdesc = sdesc_sw128(v_base + st * Cfg::kVStage, 16, 1024);
 #pragma unroll
             for (int ks = 0; ks < (D + 64) / 16; ++ks) {
               const uint64_t qd = desc_add(qdesc, (ks >> 2) * Cfg::kQBox + (ks & 3) * 32);
@@ -469,66 +472,58 @@ __global__ void __launch_bounds__(PagedCfg<D, N>::kThreads, 1) paged_decode_kern
                 umma_ss(tbase + N * sb, desc_add(kdesc, (ks >> 2) * kBox + (ks & 3) * 32), qd, id, ks ? 1u : 0u);
             }
             umma_commit(smem_u32(&sm.s_full[sb]));
-            umma_commit(smem_u32(&sm.kempty[n % KS]));
           }
-          ++seg;
         }
       } else {
-        // A = the value tile read MN-major (two 64-column boxes an M block, LBO between them), B = P^T,
-        // MN-major: 8-key atoms of 8 * 2N bytes, swizzled over the 2N bytes of a key's rows
+        // A = the value tile read MN-major (two 64-column boxes an M block, LBO between them), B = P^T, MN-major: 8-key
+        // atoms of 8 * 2N bytes, swizzled over the 2N bytes of a key's rows.  The stage is free when PV is done.
         const uint32_t id = idesc_bf16(128, N, 1, 1);
         constexpr uint32_t atom = 16 * N;
-        while (ok && cur.next(p, N, sg)) {
+        for (; cur.next(p, N, sg) && !aborted(); ++seg) {
           for (int t = sg.tile_lo; t < sg.tile_hi; ++t, ++n) {
-            const int pb = n % PS;
+            const int pb = n % PS, st = n % ST;
             const bool first = t == sg.tile_lo;
-            if (!mbar_wait(smem_u32(&sm.p_full[pb]), static_cast<uint32_t>((n / PS) & 1), wc, SB + PW_PFULL) ||
-                (first && seg > 0 && !mbar_wait(smem_u32(&sm.o_free), static_cast<uint32_t>((seg - 1) & 1), wc, SB + PW_OFREE))) {
-              ok = false;
-              break;
-            }
+            wait(sm.p_full[pb], n / PS, PW_PFULL);
+            if (t == sg.tile_lo && seg > 0) wait(sm.o_free, seg - 1, PW_OFREE);
+            if (aborted()) break;
             tc_fence_after();
             const uint32_t paddr = p_base + pb * Cfg::kPBytes;
             const uint64_t pdesc = N == 64 ? sdesc_sw128(paddr, 16, atom) : N == 32 ? sdesc_sw64(paddr, 16, atom) : sdesc_sw32(paddr, 16, atom);
 #pragma unroll
-            for (int mb = 0; mb < Cfg::kMB; ++mb) {
-              const uint64_t vdesc = sdesc_sw128(v_base + (n % VS) * Cfg::kVStage + 2 * mb * kBox, kBox, 1024);
+            for (int mb = 0; mb < MB; ++mb) {
+              const uint64_t vdesc = sdesc_sw128(v_base + st * Cfg::kVStage + 2 * mb * kBox, kBox, 1024);
 #pragma unroll
               for (int kk = 0; kk < TN / 16; ++kk)
-                umma_ss(tbase + O0 + N * mb, desc_add(vdesc, kk * 2048), desc_add(pdesc, kk * 2 * atom), id,
-                        first && kk == 0 ? 0u : 1u);
+                umma_ss(tbase + O0 + N * mb, desc_add(vdesc, kk * 2048), desc_add(pdesc, kk * 2 * atom), id, first && kk == 0 ? 0u : 1u);
             }
             umma_commit(smem_u32(&sm.o_done[pb]));
-            umma_commit(smem_u32(&sm.vempty[n % VS]));
+            umma_commit(smem_u32(&sm.empty[st]));
           }
-          ++seg;
         }
       }
       // every MMA of this thread is complete before TMEM is released (both issuers arrive)
       umma_commit(smem_u32(&sm.drain));
       uint32_t zero = 0;
       const WaitCtl dc{&zero, p.err, p.wait_limit_ns};
-      mbar_wait(smem_u32(&sm.drain), 0, dc, SB + PW_DRAIN);
+      mbar_wait(smem_u32(&sm.drain), 0, dc, kPagedSite + PW_DRAIN);
     }
-  } else if (warp >= Cfg::kConv0) {
+  } else if (warp >= 12) {
     // ================================================================== converters
-    // Warp w takes 16 keys of every tile: lanes 16 (w / 4) .. + 15 of the TMEM quadrant w % 4, the keys g and g + 8 in
-    // thread 4g + c, and of each key the 32-column chunks c + 4h and the 16-byte pieces c and c + 4 of its RoPE key, so
-    // that a warp's load covers 64 contiguous bytes of eight rows.  tcgen05.st 16x128b puts register 2j (2j + 1) of
-    // that thread at key g (g + 8), column 4j + c: the K index of QK runs through the columns in that order, and Q is
-    // stored to match.  Chunks with c & 2 are expanded second half first: eight lanes then write eight different
-    // 16-byte columns of the value tile (no bank conflicts).  The next tile's loads are issued when this one is
-    // converted; its rows were asked into L2 a tile earlier, and their page numbers one tile earlier still.
+    // Warp w takes 16 keys of every tile: lanes 16 (w / 4) .. + 15 of the TMEM quadrant w % 4.  Thread 4g + 2h + b has
+    // key g + 8b and of it the 32-column chunks h + 2m (m = 0, 1 in every 128 columns) and the 16-byte pieces h + 2m of
+    // the RoPE key, which is how tcgen05.st 16x64b spreads a warp's registers; the K index of QK runs through the
+    // columns in that order, and Q is stored to match.  The next tile's loads are issued when this one is converted;
+    // its rows were asked into L2 a tile earlier, and their page numbers one tile earlier still.
     constexpr int kKeys = kPagedTile / kPagedConv, kH = D / 128;
-    const int cw = warp - Cfg::kConv0, key0 = 32 * (cw & 3) + 16 * (cw >> 2);
-    const int g = lane >> 2, c = lane & 3;
+    const int cw = warp - 12, key0 = 32 * (cw & 3) + 16 * (cw >> 2);
+    const int rr = (lane >> 2) + 8 * (lane & 1), hf = (lane >> 1) & 1;
     const int r = p.G * D;
     const uint8_t* pool = p.pages.pool;
     const int key_at = int4_rope_at(r);
     struct Tile {
       int b, t, L, group;  // t < 0: none
     };
-    PagedCursor& walk = sm.walk[SW + cw];
+    PagedCursor& walk = sm.walk[8 + cw];
     PagedSegment& seg = sm.conv_seg[cw];
     if (lane == 0) walk = sm.cur;
     int walk_t = 0, walk_hi = 0;
@@ -540,7 +535,7 @@ __global__ void __launch_bounds__(PagedCfg<D, N>::kThreads, 1) paged_decode_kern
       }
       return Tile{seg.b, walk_t++, seg.L, seg.group};
     };
-    // this lane's key of a tile: the page is asked for here, used a tile later
+    // this lane's key of a tile (lanes 0 .. 15): the page is asked for here, used a tile later
     int page = -1, slot = 0;
     bool key_live = false;
     auto ask_page = [&](const Tile& x) {
@@ -566,97 +561,94 @@ __global__ void __launch_bounds__(PagedCfg<D, N>::kThreads, 1) paged_decode_kern
       prefetch_l2(row + key_at);
       return off;
     };
-    uint4 code[2][kH], key[2][2];
-    uint32_t scale[2][kH];
+    uint4 code[kH][2], key[4];
+    uint32_t scale[2 * kH];  // of the chunks 2m and 2m + 1
     auto load_rows = [&](long long off, int group) {
-      const uint8_t* cp = pool + 16 * c + group * (D / 2);
-      const uint8_t* sp = pool + 2 * c + r / 2 + group * (D / 16);
-      const uint8_t* kp = pool + 16 * c + key_at;
-      if (__all_sync(0xffffffffu, off >= 0 || lane >= kKeys)) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const long long at = __shfl_sync(0xffffffffu, off, 8 * k + g);
-          static_for<kH>([&](auto h) { code[k][h] = ldg16<64 * h>(cp + at); });
-          static_for<kH>([&](auto h) { scale[k][h] = ldg2<8 * h>(sp + at); });
-          static_for<2>([&](auto h) { key[k][h] = ldg16<64 * h>(kp + at); });
+      const long long at = __shfl_sync(0xffffffffu, off, rr);
+      const uint8_t* cp = pool + at + (16 * hf + group * (D / 2));
+      const uint8_t* sp = pool + at + (r / 2 + group * (D / 16));
+      const uint8_t* kp = pool + at + (16 * hf + key_at);
+      if (__all_sync(0xffffffffu, at >= 0) || at >= 0) {
+        static_for<kH>([&](auto h) {
+          code[h][0] = ldg16<64 * h>(cp);
+          code[h][1] = ldg16<64 * h + 32>(cp);
+        });
+        if constexpr (D == 128) {
+          const uint2 v = ldg8(sp);
+          scale[0] = v.x, scale[1] = v.y;
+        } else {
+          static_for<kH / 2>([&](auto h) {
+            const uint4 v = ldg16<16 * h>(sp);
+            scale[4 * h] = v.x, scale[4 * h + 1] = v.y, scale[4 * h + 2] = v.z, scale[4 * h + 3] = v.w;
+          });
         }
-      } else {  // rows without a token: codes 0 times scale 0, and a key of zeros
+        static_for<4>([&](auto m) { key[m] = ldg16<32 * m>(kp); });
+      } else {  // no token: scales of 0 make any codes zeros, and the key is zeros
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const long long at = __shfl_sync(0xffffffffu, off, 8 * k + g);
-          static_for<kH>([&](auto h) { code[k][h] = ldg16_if<64 * h>(cp + at, at >= 0); });
-          static_for<kH>([&](auto h) { scale[k][h] = ldg2_if<8 * h>(sp + at, at >= 0); });
-          static_for<2>([&](auto h) { key[k][h] = ldg16_if<64 * h>(kp + at, at >= 0); });
-        }
+        for (int m = 0; m < 2 * kH; ++m) scale[m] = 0;
+#pragma unroll
+        for (int m = 0; m < 4; ++m) key[m] = make_uint4(0u, 0u, 0u, 0u);
       }
     };
     uint32_t mask = 0x000f000fu, magic = 0x43004300u;
     asm volatile("" : "+r"(mask), "+r"(magic));
-    // where word e of this lane's chunk goes in the value tile (key g + 8: 1024 bytes on)
-    uint32_t at_word[4];
+    const uint32_t pick = hf ? 0x3232u : 0x1010u;  // this lane's scale of a pair, twice
+    const int vrow = key0 + paged_key_row<Cfg::kTS>(rr);
+    uint32_t at_word[4];  // where word e of this lane's chunk goes in the value tile
 #pragma unroll
-    for (int e = 0; e < 4; ++e) at_word[e] = (key0 + g) * 128 + (c >> 1) * kBox + (((4 * (c & 1) + (e ^ (c & 2))) ^ g) << 4);
+    for (int e = 0; e < 4; ++e) at_word[e] = vrow * 128 + (((4 * hf + e) ^ (vrow & 7)) << 4);
     const uint32_t tlane = tbase + K0 + (static_cast<uint32_t>(key0) << 16);
+#pragma unroll
+    for (int h = 0; h < kH; ++h) code[h][0] = code[h][1] = make_uint4(0u, 0u, 0u, 0u);
     Tile now = next_tile(), then = Tile{0, -1, 0, 0};
     ask_page(now);
-    long long off = row_of_page(now), off_then = -1;
+    long long off_then = row_of_page(now);
     if (now.t >= 0) {
-      load_rows(off, now.group);
+      load_rows(off_then, now.group);
       then = next_tile();
     }
     ask_page(then);
-    if (then.t >= 0) off_then = row_of_page(then);
+    off_then = row_of_page(then);
     Tile later = then.t >= 0 ? next_tile() : then;
     ask_page(later);
     for (int n = 0; now.t >= 0; ++n) {
-      if ((n >= KS && !wait_all(sm.kempty[n % KS], n / KS - 1, PW_KEMPTY)) ||
-          (n >= VS && !wait_all(sm.vempty[n % VS], n / VS - 1, PW_VEMPTY)))
-        break;
-      uint8_t* stage = dsm + (n % VS) * Cfg::kVStage;
-      const uint32_t ktm = tlane + (n % KS) * Cfg::kKCols;
+      const int st = n % ST;
+      if (n >= ST) wait(sm.empty[st], n / ST - 1, PW_EMPTY);
       tc_fence_after();
+      uint8_t* stage = dsm + st * Cfg::kVStage;
+      const uint32_t ktm = tlane + st * Cfg::kKCols;
 #pragma unroll
       for (int h = 0; h < kH; ++h) {
         uint32_t out[32];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t s2 = __byte_perm(scale[k][h], 0, 0x1010);
+        for (int m = 0; m < 2; ++m) {
+          const uint32_t s2 = __byte_perm(scale[2 * h + m], 0, pick);
           const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&s2);
           const __nv_bfloat162 o = __hmul2(s, __float2bfloat162_rn(-136.f));
-          const uint4 v = code[k][h];
-          const bool swap = (c & 2) != 0;
-          const uint32_t word[4] = {swap ? v.z : v.x, swap ? v.w : v.y, swap ? v.x : v.z, swap ? v.y : v.w};
+          const uint32_t word[4] = {code[h][m].x, code[h][m].y, code[h][m].z, code[h][m].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint4 x = int4_expand(word[e], mask, magic, s, o);
-            *reinterpret_cast<uint4*>(stage + at_word[e] + 2 * h * kBox + 1024 * k) = x;
-            out[8 * e + k] = x.x;
-            out[8 * e + 2 + k] = x.y;
-            out[8 * e + 4 + k] = x.z;
-            out[8 * e + 6 + k] = x.w;
+            *reinterpret_cast<uint4*>(stage + at_word[e] + (2 * h + m) * kBox) = x;
+            out[16 * m + 4 * e] = x.x;
+            out[16 * m + 4 * e + 1] = x.y;
+            out[16 * m + 4 * e + 2] = x.z;
+            out[16 * m + 4 * e + 3] = x.w;
           }
         }
-        if (Cfg::kTS) tmem_st_16x128_x16(ktm + 64 * h, out);
+        if (Cfg::kTS) tmem_st_16x64_x32(ktm + 64 * h, out);
       }
       {
         uint32_t out[16];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            out[8 * h + k] = key[k][h].x;
-            out[8 * h + 2 + k] = key[k][h].y;
-            out[8 * h + 4 + k] = key[k][h].z;
-            out[8 * h + 6 + k] = key[k][h].w;
-          }
-        }
-        tmem_st_16x128_x8(ktm + (Cfg::kTS ? D / 2 : 0), out);
+        for (int m = 0; m < 4; ++m) out[4 * m] = key[m].x, out[4 * m + 1] = key[m].y, out[4 * m + 2] = key[m].z, out[4 * m + 3] = key[m].w;
+        tmem_st_16x64_x16(ktm + (Cfg::kTS ? D / 2 : 0), out);
       }
-      if (then.t >= 0) load_rows(off_then, then.group);
       tmem_wait_st();
-      fence_proxy_async_smem();
+      fence_proxy_async_smem();  // ahead of the loads: its memory barrier would wait for them
       tc_fence_before();
-      warp_arrive(sm.full[n % VS]);
+      warp_arrive(sm.full[st]);
+      if (then.t >= 0) load_rows(off_then, then.group);
       now = then;
       then = later;
       off_then = row_of_page(then);
@@ -664,27 +656,26 @@ __global__ void __launch_bounds__(PagedCfg<D, N>::kThreads, 1) paged_decode_kern
       ask_page(later);
     }
   } else if (warp >= 4) {
-    // ================================================================== softmax / epilogue
+    // ================================================================== softmax / epilogue (warps 2 and 3 are idle)
     const int sw = warp - 4;
-    const int q4 = warp & 3;                   // TMEM lane quadrant
-    const int hh = sw >> 2, rb = RW * hh;      // rows rb .. rb + RW - 1 of the unit
-    const int k = q4 * 32 + lane;              // key of the tile; value column (of an M block) of O^T
-    const int rl = lane % RW;                  // this lane's row, rb + rl, after a reduction over lanes
-    const uint32_t tlane = tbase + (static_cast<uint32_t>(q4 * 32) << 16);
+    const int q4 = warp & 3;                     // TMEM lane quadrant
+    const int half = sw >> 2, rb = RW * half;    // rows rb .. rb + RW - 1 of the unit
+    const int k = q4 * 32 + lane;                // key of the tile; value column (of an M block) of O^T
+    const int rl = lane % RW;                    // this lane's row, rb + rl, after a reduction over lanes
+    const uint32_t tlane = tbase + (static_cast<uint32_t>(q4 * 32) << 16) + rb;
     int xc = 0, vc = 0;
     // every warp posts one value per row (lanes 0 .. RW - 1) and reads the posts of the four warps with its rows
-    auto exchange = [&](float v, float (&all)[4]) -> bool {
+    auto exchange = [&](float v, float (&all)[4]) {
       const int b = xc & 1;
       if (lane < RW) sm.red[b][sw][lane] = v;
       warp_arrive(sm.xchg_bar);
-      const bool okx = wait_all(sm.xchg_bar, xc, PW_XCHG);
+      wait(sm.xchg_bar, xc, PW_XCHG);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) all[w] = sm.red[b][4 * hh + w][rl];
+      for (int w = 0; w < 4; ++w) all[w] = sm.red[b][4 * half + w][rl];
       ++xc;
-      return okx;
     };
     auto load_q = [&](const PagedSegment& s) {
-      paged_load_q<D, N, 32 * SW>(p, s, qsm, sw * 32 + lane);
+      paged_load_q<D, N>(p, s, qsm, sw * 32 + lane, 256);
       warp_arrive(sm.q_ready);
     };
 
@@ -693,85 +684,82 @@ __global__ void __launch_bounds__(PagedCfg<D, N>::kThreads, 1) paged_decode_kern
       if (__ldg(p.pages.seq_lens + b) > 0) continue;
       const size_t rows = static_cast<size_t>(p.s_q) * p.h_q;
       uint4* o = reinterpret_cast<uint4*>(p.out + b * rows * D);
-      for (size_t e = sw * 32 + lane; e < rows * D / 8; e += 32 * SW) o[e] = make_uint4(0u, 0u, 0u, 0u);
-      for (size_t e = sw * 32 + lane; e < rows; e += 32 * SW) p.lse[b * rows + e] = -INFINITY;
+      for (size_t e = sw * 32 + lane; e < rows * D / 8; e += 256) o[e] = make_uint4(0u, 0u, 0u, 0u);
+      for (size_t e = sw * 32 + lane; e < rows; e += 256) p.lse[b * rows + e] = -INFINITY;
     }
 
+    // where this key's weights go: 2N bytes a key, 16-byte chunk c at c ^ the swizzle of that width
+    const int krow = paged_key_row<Cfg::kTS>(k);
+    const int x8 = N == 64 ? (krow & 7) : N == 32 ? ((krow >> 1) & 3) : ((krow >> 2) & 1);
+    uint8_t* prow0 = psm + krow * (2 * N);
     PagedCursor& walk = sm.walk[sw];
     if (lane == 0) walk = sm.cur;
-    bool ok = true;
-    int n = 0, seg = 0;
-    float m_run = 0.f;  // reference of row rb + rl (log2 units)
-    float l[RW];        // this key lane's share of each row's sum of weights
+    int n0 = 0, seg = 0;  // the tile count at the segment's start
+    float l[RW];          // this key lane's share of each row's sum of weights
     bool have = paged_next(p, N, walk, sm.seg[sw][0], lane);
     if (have) load_q(sm.seg[sw][0]);
-    for (; ok && have; ++seg) {
+    for (; have; ++seg) {
       const PagedSegment& sg = sm.seg[sw][seg & 1];
       PagedSegment& nx = sm.seg[sw][(seg + 1) & 1];
-      bool have_nx = false;
-      const int t_lo = sg.tile_lo, t_hi = sg.tile_hi;
-      const int lim0 = sg.L - p.s_q;               // query i sees keys 0 .. lim0 + i
-      const int newest = p.hpg - (sg.row0 + rb);   // rows from here on are query 1's (or padding)
-      for (int t = t_lo; t < t_hi; ++t, ++n) {
-        const int sb = n % SS, pb = n % PS;
-        const bool first = t == t_lo;
-        if (!wait_all(sm.s_full[sb], n / SS, PW_SFULL)) {
-          ok = false;
-          break;
-        }
+      const int tiles = sg.tile_hi - sg.tile_lo;
+      const int lim0 = sg.L - p.s_q - sg.tile_lo * TN - k;  // query i sees this thread's key of tile j where 128 j <= lim0 + i
+      const int whole = lim0 + k - (TN - 1);                // 128 j <= whole: every query sees all keys of the tile
+      const int newest = p.hpg - (sg.row0 + rb);            // rows from here on are query 1's (or padding)
+      float m_run = 0.f;                                    // reference of row rb + rl (log2 units)
+#pragma unroll
+      for (int j = 0; j < RW; ++j) l[j] = 0.f;
+      for (int j = 0; j < tiles; ++j) {
+        const int n = n0 + j, sb = n % SS, pb = n % PS;
+        const bool first = j == 0;
+        wait(sm.s_full[sb], n / SS, PW_SFULL);
         tc_fence_after();
         // the tile's scores, -inf where the row does not see the key
         float x[RW];
-        tmem_load_rows<RW>(tlane + N * sb + rb, x);
+        tmem_load_rows<RW>(tlane + N * sb, x);
         tmem_wait_ld();
         tc_fence_before();
         warp_arrive(sm.s_free[sb]);
-        if ((t + 1) * TN - 1 > lim0) {
-          const int ahead = t * TN + k - lim0;
+        if (TN * j > whole) {
+          const int ahead = TN * j - lim0;
 #pragma unroll
-          for (int j = 0; j < RW; ++j)
-            if (ahead > (j >= newest ? 1 : 0)) x[j] = -INFINITY;
+          for (int i = 0; i < RW; ++i)
+            if (ahead > (i >= newest ? 1 : 0)) x[i] = -INFINITY;
         }
         bool raise = first;
         if (first) {
 #pragma unroll
-          for (int j = 0; j < RW; ++j) x[j] *= p.sl2;
+          for (int i = 0; i < RW; ++i) x[i] *= p.sl2;
         } else {
           float top = -INFINITY;
 #pragma unroll
-          for (int j4 = 0; j4 < RW / 4; ++j4) {
-            const float4 r4 = reinterpret_cast<const float4*>(sm.ref[sw])[j4];
-            x[4 * j4] = fmaf(x[4 * j4], p.sl2, -r4.x);
-            x[4 * j4 + 1] = fmaf(x[4 * j4 + 1], p.sl2, -r4.y);
-            x[4 * j4 + 2] = fmaf(x[4 * j4 + 2], p.sl2, -r4.z);
-            x[4 * j4 + 3] = fmaf(x[4 * j4 + 3], p.sl2, -r4.w);
-            top = fmaxf(top, fmaxf(fmaxf(x[4 * j4], x[4 * j4 + 1]), fmaxf(x[4 * j4 + 2], x[4 * j4 + 3])));
+          for (int i = 0; i < RW; i += 4) {
+            const float4 r4 = *reinterpret_cast<const float4*>(&sm.ref[sw][i]);
+            x[i] = fmaf(x[i], p.sl2, -r4.x);
+            x[i + 1] = fmaf(x[i + 1], p.sl2, -r4.y);
+            x[i + 2] = fmaf(x[i + 2], p.sl2, -r4.z);
+            x[i + 3] = fmaf(x[i + 3], p.sl2, -r4.w);
+            top = fmaxf(top, fmaxf(fmaxf(x[i], x[i + 1]), fmaxf(x[i + 2], x[i + 3])));
           }
           // The flag of vote vc is one of three words: it is cleared after vote vc + 1, when every warp has read
           // it, and set again for vote vc + 3 by warps that passed vote vc + 2, which this warp joins after clearing.
-          if (__any_sync(0xffffffffu, top > kPagedRaise) && lane == 0) *const_cast<volatile uint32_t*>(&sm.vote[vc % 3]) = 1u;
+          volatile uint32_t* flag = sm.vote;
+          if (__any_sync(0xffffffffu, top > kPagedRaise) && lane == 0) flag[vc % 3] = 1u;
           warp_arrive(sm.vote_bar);
-          if (!wait_all(sm.vote_bar, vc, PW_VOTE)) {
-            ok = false;
-            break;
-          }
-          raise = *const_cast<volatile uint32_t*>(&sm.vote[vc % 3]) != 0;  // the same for all softmax warps
-          if (sw == 0 && lane == 0) *const_cast<volatile uint32_t*>(&sm.vote[(vc + 2) % 3]) = 0u;
+          wait(sm.vote_bar, vc, PW_VOTE);
+          raise = flag[vc % 3] != 0;  // the same for all softmax warps
+          if (sw == 0 && lane == 0) flag[(vc + 2) % 3] = 0u;
           ++vc;
         }
         if (raise) {
           // the rows' maxima over the tile's keys, above the references (the first tile's references are 0)
           float mw = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < RW; ++j) {
-            const float v = warp_max(x[j]);
-            if (rl == j) mw = v;
+          for (int i = 0; i < RW; ++i) {
+            const float v = warp_max(x[i]);
+            if (rl == i) mw = v;
           }
           float all[4];
-          if (!exchange(mw, all)) {
-            ok = false;
-            break;
-          }
+          exchange(mw, all);
           const float mt = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
           // a row that sees no key of the segment's first tile sees none of its later ones: its reference stays 0
           const float up = first ? (mt == -INFINITY ? 0.f : mt) : fmaxf(mt, 0.f);
@@ -782,84 +770,65 @@ __global__ void __launch_bounds__(PagedCfg<D, N>::kThreads, 1) paged_decode_kern
           }
           __syncwarp();
 #pragma unroll
-          for (int j = 0; j < RW; ++j) {
-            const float u = *const_cast<volatile float*>(&sm.fac[sw][j]);
-            x[j] -= u;
-            l[j] = first ? 0.f : l[j] * ex2_approx(-u);
+          for (int i = 0; i < RW; ++i) {
+            const float u = *const_cast<volatile float*>(&sm.fac[sw][i]);
+            x[i] -= u;
+            l[i] = first ? 0.f : l[i] * ex2_approx(-u);
           }
         }
-        if (t == t_hi - 1 && (have_nx = paged_next(p, N, walk, nx, lane))) load_q(nx);  // this unit's QKs are done
         uint32_t pw[RW / 2];
 #pragma unroll
-        for (int j = 0; j < RW / 2; ++j) {
-          const float e0 = ex2_approx(x[2 * j]), e1 = ex2_approx(x[2 * j + 1]);
-          l[2 * j] += e0;
-          l[2 * j + 1] += e1;
-          pw[j] = pack_bf16x2(e0, e1);
+        for (int i = 0; i < RW / 2; ++i) {
+          const float e0 = ex2_approx(x[2 * i]), e1 = ex2_approx(x[2 * i + 1]);
+          l[2 * i] += e0;
+          l[2 * i + 1] += e1;
+          pw[i] = pack_bf16x2(e0, e1);
         }
         // P buffer pb was last read by PV(n - PS)
-        if (n >= PS && !wait_all(sm.o_done[pb], n / PS - 1, PW_ODONE)) {
-          ok = false;
-          break;
-        }
-        {
-          // a key's rows are 2N bytes; 16-byte chunk c lies at c ^ the swizzle of that width
-          uint8_t* prow = psm + pb * Cfg::kPBytes + k * (2 * N);
-          const int x8 = N == 64 ? (k & 7) : N == 32 ? ((k >> 1) & 3) : ((k >> 2) & 1);
+        if (n >= PS) wait(sm.o_done[pb], n / PS - 1, PW_ODONE);
+        uint8_t* prow = prow0 + pb * Cfg::kPBytes;
 #pragma unroll
-          for (int c = 0; c < RW / 8; ++c)
-            *reinterpret_cast<uint4*>(prow + (((hh * (RW / 8) + c) ^ x8) << 4)) =
-                make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
-        }
+        for (int c = 0; c < RW / 8; ++c)
+          *reinterpret_cast<uint4*>(prow + ((((rb / 8) + c) ^ x8) << 4)) =
+              make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
         fence_proxy_async_smem();
         if (raise && !first) {
-          // O^T holds the segment's tiles up to n - 1
-          if (!wait_all(sm.o_done[(n - 1) % PS], (n - 1) / PS, PW_ODONE)) {
-            ok = false;
-            break;
-          }
+          // O^T holds the segment's tiles up to the one before
+          wait(sm.o_done[(n - 1) % PS], (n - 1) / PS, PW_ODONE);
           tc_fence_after();
-          paged_rescale<RW, N, Cfg::kMB>(tlane + O0 + rb, sm.fac[sw]);
+          paged_rescale<RW, N, MB>(tlane + O0, sm.fac[sw]);
         }
         tc_fence_before();
         warp_arrive(sm.p_full[pb]);
-        if (t != t_hi - 1) continue;
-        // ---------------------------------------------------------------- the segment's end
-        const float lw = paged_rows_reduce<false, RW>(l, lane);
-        float lt[4];
-        if (!exchange(lw, lt)) {
-          ok = false;
-          break;
-        }
-        const float lsum = (lt[0] + lt[1]) + (lt[2] + lt[3]);
-        // a NaN sum stays NaN in both results
-        const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-        const float lse = lsum == 0.f ? -INFINITY : (m_run + log2f(lsum)) * 0.69314718055994531f;
-        __syncwarp();
-        if (lane < RW) sm.fac[sw][lane] = inv;
-        __syncwarp();
-        if (!wait_all(sm.o_done[pb], n / PS, PW_ODONE)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const size_t part = static_cast<size_t>(2 * range + (sg.slot < 0 ? 0 : sg.slot)) * N;
-        paged_store_out<D, N, RW, Cfg::kMB>(p, sg, tlane + O0 + rb, sm.fac[sw], rb, k, part);
-        const size_t out0 = static_cast<size_t>(sg.b) * p.s_q * p.h_q + sg.group * p.hpg;
-        if (q4 == 0 && lane < RW) {
-          const int g = sg.row0 + rb + lane;
-          if (g < p.R) {
-            const int i = g >= p.hpg;
-            if (sg.slot < 0)
-              p.lse[out0 + static_cast<size_t>(i) * p.h_q + (g - i * p.hpg)] = lse;
-            else
-              p.part_lse[part + rb + lane] = lse;
-          }
-        }
-        if (sg.slot >= 0 && sw == 0 && lane == 0) p.seg_info[2 * range + sg.slot] = 4 * sg.unit + sg.first + 2 * sg.last;
-        tc_fence_before();
-        warp_arrive(sm.o_free);
       }
+      // ---------------------------------------------------------------- the segment's end
+      const int n_last = n0 + tiles - 1;
+      const bool have_nx = paged_next(p, N, walk, nx, lane);
+      if (have_nx) load_q(nx);  // the unit's QKs are done
+      float lt[4];
+      exchange(paged_rows_reduce<false, RW>(l, lane), lt);
+      const float lsum = (lt[0] + lt[1]) + (lt[2] + lt[3]);  // a NaN stays one in both results
+      __syncwarp();
+      if (lane < RW) {
+        sm.fac[sw][lane] = lsum == 0.f ? 0.f : 1.f / lsum;
+        const int g = sg.row0 + rb + lane;
+        if (q4 == 0 && g < p.R) {
+          const float lse = lsum == 0.f ? -INFINITY : (m_run + log2f(lsum)) * 0.69314718055994531f;
+          const int i = g >= p.hpg;
+          if (sg.slot < 0)
+            p.lse[(static_cast<size_t>(sg.b) * p.s_q + i) * p.h_q + sg.group * p.hpg + (g - i * p.hpg)] = lse;
+          else
+            p.part_lse[static_cast<size_t>(2 * range + sg.slot) * N + rb + lane] = lse;
+        }
+      }
+      __syncwarp();
+      wait(sm.o_done[n_last % PS], n_last / PS, PW_ODONE);
+      tc_fence_after();
+      paged_store_out<D, N, RW>(p, sg, tlane + O0, sm.fac[sw], rb, k, static_cast<size_t>(2 * range + (sg.slot < 0 ? 0 : sg.slot)) * N);
+      if (sg.slot >= 0 && sw == 0 && lane == 0) p.seg_info[2 * range + sg.slot] = 4 * sg.unit + sg.first + 2 * sg.last;
+      tc_fence_before();
+      warp_arrive(sm.o_free);
+      n0 += tiles;
       have = have_nx;
     }
   }
