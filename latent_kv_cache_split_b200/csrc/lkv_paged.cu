@@ -8,6 +8,7 @@
 #include "../../include/lkv.h"
 #include "lkv_int4.cuh"
 #include "lkv_paged_decode.cuh"
+#include "lkv_paged_warp.cuh"
 #include "lkv_rope.cuh"
 
 lkv_status lkv_internal_device_info(int** err, int* num_sms, unsigned long long* wait_ns);  // lkv_api.cu
@@ -68,7 +69,7 @@ void launch_rope(const RopeParams& p, bool interleaved, unsigned blocks, cudaStr
 
 // Rows of a unit (the MMA's N): the smallest of 16, 32, 64 that holds a group's rows, so that small groups
 // spend no softmax on padding; 64 at most, and a group of more rows is several units that read the same tiles.
-int paged_rows(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }
+int paged_rows(int R, int d) { return R <= 16 || (d == 128 && R <= 32) || d == 256 ? 16 : R <= 32 ? 32 : 64; }
 
 struct PagedPlan {
   int N, RB, U, P, lockstep;
@@ -77,7 +78,7 @@ struct PagedPlan {
 
 void paged_plan(PagedPlan* w, int s_q, int h_q, int groups, int d, int num_sms) {
   const int R = s_q * (h_q / groups);
-  w->N = paged_rows(R);
+  w->N = paged_rows(R, d);
   w->RB = (R + w->N - 1) / w->N;
   w->U = groups * w->RB;
   // Units in lockstep share a request's RoPE keys and scales through L2; not where that leaves more than a
@@ -96,23 +97,33 @@ void paged_plan(PagedPlan* w, int s_q, int h_q, int groups, int d, int num_sms) 
 
 // The decode kernel, then the combine as its programmatic dependent: its launch overlaps the decode, and its
 // blocks wait for the decode's completion before they read the partials.
-template <int D, int N>
-lkv_status launch_decode(const PagedDecodeParams& p, cudaStream_t s) {
-  using Cfg = PagedCfg<D, N>;
-  static bool ready[kMaxDevices];  // the kernel's attribute is set on a device once
+// A kernel's dynamic shared memory is an attribute, set on each device once.
+template <class Kernel>
+lkv_status allow_smem(Kernel k, size_t bytes, bool (&ready)[kMaxDevices]) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return LKV_ERR_CUDA;
   if (!ready[dev]) {
-    if (cudaFuncSetAttribute(paged_decode_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(Cfg::kSmem)) != cudaSuccess) {
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess) {
       cudaGetLastError();
       return LKV_ERR_CUDA;
     }
     ready[dev] = true;
   }
-  paged_decode_kernel<D, N><<<p.P, kPagedThreads, Cfg::kSmem, s>>>(p);
-  const lkv_status st = launched();
-  if (st != LKV_OK) return st;
+  return LKV_OK;
+}
+
+template <int D, int N>
+lkv_status launch_decode(const PagedDecodeParams& p, cudaStream_t s) {
+  static bool ready[kMaxDevices];
+  lkv_status st;
+  if constexpr (N == kWarpRows && D <= 256) {
+    if ((st = allow_smem(paged_warp_kernel<D>, WarpCfg<D>::kSmem, ready)) != LKV_OK) return st;
+    paged_warp_kernel<D><<<p.P, kWarpThreads, WarpCfg<D>::kSmem, s>>>(p);
+  } else {
+    if ((st = allow_smem(paged_decode_kernel<D, N>, PagedCfg<D, N>::kSmem, ready)) != LKV_OK) return st;
+    paged_decode_kernel<D, N><<<p.P, kPagedThreads, PagedCfg<D, N>::kSmem, s>>>(p);
+  }
+  if ((st = launched()) != LKV_OK) return st;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.P, (N + kPagedCombineWarps - 1) / kPagedCombineWarps);
   cfg.blockDim = dim3(kPagedCombineWarps * 32);
@@ -123,8 +134,8 @@ lkv_status launch_decode(const PagedDecodeParams& p, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_combine_kernel<D, N>, p);
-  const lkv_status after = launched();
-  return e == cudaSuccess ? after : LKV_ERR_CUDA;
+  st = launched();
+  return e == cudaSuccess ? st : LKV_ERR_CUDA;
 }
 
 lkv_status launch_decode_for(const PagedDecodeParams& p, int d, int N, cudaStream_t s) {

@@ -199,6 +199,7 @@ __device__ __noinline__ bool paged_next(const PagedDecodeParams& p, int rows, Pa
   int ok = 0;
   __syncwarp();
   if (lane == 0) ok = walk.next(p, rows, out);
+  __syncwarp();
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
