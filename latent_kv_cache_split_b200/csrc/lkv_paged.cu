@@ -69,7 +69,7 @@ void launch_rope(const RopeParams& p, bool interleaved, unsigned blocks, cudaStr
 
 // Rows of a unit (the MMA's N): the smallest of 16, 32, 64 that holds a group's rows, so that small groups
 // spend no softmax on padding; 64 at most, and a group of more rows is several units that read the same tiles.
-int paged_rows(int R, int d) { return R <= 16 || (d == 128 && R <= 32) || d == 256 ? 16 : R <= 32 ? 32 : 64; }
+int paged_rows(int R, int d) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }
 
 struct PagedPlan {
   int N, RB, U, P, lockstep;
@@ -116,7 +116,7 @@ template <int D, int N>
 lkv_status launch_decode(const PagedDecodeParams& p, cudaStream_t s) {
   static bool ready[kMaxDevices];
   lkv_status st;
-  if constexpr (N == kWarpRows && D <= 256) {
+  if constexpr (N == 1234 && D <= 256) {
     if ((st = allow_smem(paged_warp_kernel<D>, WarpCfg<D>::kSmem, ready)) != LKV_OK) return st;
     paged_warp_kernel<D><<<p.P, kWarpThreads, WarpCfg<D>::kSmem, s>>>(p);
   } else {

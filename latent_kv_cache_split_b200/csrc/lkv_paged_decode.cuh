@@ -31,7 +31,8 @@
 namespace lkv {
 
 constexpr int kPagedConv = 8;                          // converter warps
-constexpr int kPagedThreads = 32 * (4 + 8 + kPagedConv);  // issuers, softmax, converters
+constexpr int kPagedSoft = 16;                         // softmax warps
+constexpr int kPagedThreads = 32 * (4 + kPagedSoft + kPagedConv);  // issuers, softmax, converters
 constexpr int kPagedTile = 128;
 constexpr float kPagedRaise = 64.f;  // log2 units a score may pass its row's reference by
 
@@ -161,37 +162,43 @@ struct PagedCfg {
   static constexpr bool kTS = D <= 256;
   static constexpr int kKCols = (kTS ? D / 2 : 0) + 32;  // TMEM columns of a stage: the key operand
   static constexpr int kStages = D == 128 ? 3 : D == 256 ? 2 : 1;
-  static constexpr int kRW = N / 2;  // rows of a softmax warp: two sets of four warps, one warp for each TMEM lane quadrant
+  // Softmax: sets of four warps, one for each TMEM lane quadrant, with kRW rows each; at N <= 32 two groups of two sets
+  // take turns at the tiles, each with accumulators, references and sums of its own, joined at the segment's end (a
+  // group is bound by the latency of its chain of instructions, not by their number).
+  static constexpr int kGroups = N == 64 ? 1 : 2;
+  static constexpr int kGW = kPagedSoft / kGroups;  // warps of a group
+  static constexpr int kRW = 4 * N / kGW;           // rows of a softmax warp
   static constexpr int kSBufs = D == 256 && N == 64 ? 1 : 2;  // S^T buffers
   static constexpr int kPs = D == 512 && N == 64 ? 1 : 2;     // P buffers
   static constexpr int kQBox = N * 128;
   static constexpr int kQBytes = (kVBoxes + 1) * kQBox;
   static constexpr int kPBytes = kPagedTile * N * 2;
   static constexpr int kMB = D / 128;            // M blocks of PV
-  static constexpr uint32_t kO0 = kSBufs * N, kK0 = (kO0 + kMB * N + 31) / 32 * 32;  // TMEM: S^T buffers, O^T, key stages
+  static constexpr uint32_t kO0 = kSBufs * N, kK0 = (kO0 + kGroups * kMB * N + 31) / 32 * 32;  // TMEM: S^T buffers, O^T, key stages
   static constexpr int kTmemNeed = kK0 + kStages * kKCols;
   static constexpr int kTmemCols = kTmemNeed <= 128 ? 128 : kTmemNeed <= 256 ? 256 : 512;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kVStage + kQBytes + kPs * kPBytes;
   static_assert(kTmemNeed <= 512, "TMEM budget");
-  static_assert(kSmem <= 232448 - 8192, "shared memory budget");
 };
 
 constexpr int kPagedSite = LKV_SITE_WAIT_BASE + 300;  // wait sites of this kernel
-enum PagedWaitSite { PW_EMPTY = 1, PW_FULL, PW_SFREE, PW_QREADY, PW_PFULL, PW_OFREE, PW_SFULL, PW_ODONE, PW_VOTE, PW_XCHG, PW_DRAIN };
+enum PagedWaitSite { PW_EMPTY = 1, PW_FULL, PW_SFREE, PW_QREADY, PW_PFULL, PW_OFREE, PW_SFULL, PW_ODONE, PW_VOTE, PW_XCHG, PW_FIN, PW_DRAIN };
 
-template <int RW>
+template <int RW, int N, int NG>
 struct __align__(16) PagedSmem {
   uint64_t full[3], empty[3];
   uint64_t s_full[2], s_free[2], p_full[2], o_done[2];
-  uint64_t q_ready, o_free, vote_bar, xchg_bar, drain;
-  alignas(16) float red[2][8][RW];    // [buffer][softmax warp][its row]
-  alignas(16) float ref[8][RW];       // per softmax warp: its rows' references (log2 units)
-  alignas(16) float fac[8][RW];       // per softmax warp: what the references rose by, then 1 / l
-  uint32_t vote[3];
+  uint64_t vote_bar[2], xchg_bar[2];  // of a softmax group
+  uint64_t q_ready, o_free, fin_bar, drain;
+  alignas(16) float red[2][kPagedSoft][RW];  // [buffer][softmax warp][its row]
+  alignas(16) float ref[kPagedSoft][RW];     // per softmax warp: its rows' references (log2 units)
+  alignas(16) float fin_m[2][NG][N], fin_l[2][NG][N];  // [segment parity][group][row]: reference and sum at the segment's end
+  alignas(16) float fac[kPagedSoft][NG][RW];  // per softmax warp: what the references rose by; then the groups' factors
+  uint32_t vote[2][3];
   uint32_t tmem_base, abort;
   // Walk state of the warps that run out of registers first: read where it is needed.
-  PagedCursor cur, walk[8 + kPagedConv];
-  PagedSegment seg[8][2], conv_seg[kPagedConv];
+  PagedCursor cur, walk[kPagedSoft + kPagedConv];
+  PagedSegment seg[kPagedSoft][2], conv_seg[kPagedConv];
 };
 
 // The next segment of a warp's own walk, both in shared memory; the same answer in every lane.
@@ -358,26 +365,35 @@ __device__ __noinline__ void paged_rescale(uint32_t tmem, const float* up) {
   tmem_wait_st();
 }
 
-// O^T times 1 / l: the result, or the range's partial.  c: this thread's value column of an M block.
+// The groups' O^T times their factors, summed: the result, or the range's partial.  tmem: the first of this warp's rows
+// in group 0's accumulators; used: bit g set where group g had a tile; c: this thread's value column of an M block.
 template <int D, int N, int RW>
-__device__ __noinline__ void paged_store_out(const PagedDecodeParams& p, const PagedSegment& s, uint32_t tmem, const float* inv, int rb,
-                                             int c, size_t part) {
+__device__ __noinline__ void paged_store_out(const PagedDecodeParams& p, const PagedSegment& s, uint32_t tmem, const float* fac, int used,
+                                             int rb, int c, size_t part) {
   const int n = min(RW, p.R - (s.row0 + rb));
   const size_t row0 = static_cast<size_t>(s.b) * p.s_q * p.h_q + s.group * p.hpg;
 #pragma unroll 1
   for (int mb = 0; mb < D / 128; ++mb, c += 128) {
     float o[RW];
-    tmem_load_rows<RW>(tmem + N * mb, o);
-    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < RW; ++j) o[j] = 0.f;
+#pragma unroll 1
+    for (int g = 0; g < 2; ++g) {
+      if (!(used >> g & 1)) continue;
+      float v[RW];
+      tmem_load_rows<RW>(tmem + N * (D / 128 * g + mb), v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < RW; ++j) o[j] = fmaf(v[j], fac[RW * g + j], o[j]);
+    }
 #pragma unroll
     for (int j = 0; j < RW; ++j) {
       if (j >= n) break;
       const int g = s.row0 + rb + j;
-      const float v = o[j] * inv[j];
       if (s.slot < 0)
-        p.out[(row0 + (g >= p.hpg ? p.h_q + g - p.hpg : g)) * D + c] = __float2bfloat16_rn(v);
+        p.out[(row0 + (g >= p.hpg ? p.h_q + g - p.hpg : g)) * D + c] = __float2bfloat16_rn(o[j]);
       else
-        p.part_o[(part + rb + j) * D + c] = v;
+        p.part_o[(part + rb + j) * D + c] = o[j];
     }
   }
 }
@@ -386,12 +402,13 @@ template <int D, int N>
 __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
   using Cfg = PagedCfg<D, N>;
   constexpr int TN = kPagedTile, ST = Cfg::kStages, SS = Cfg::kSBufs, PS = Cfg::kPs;
-  constexpr int RW = Cfg::kRW, MB = Cfg::kMB;
+  constexpr int RW = Cfg::kRW, MB = Cfg::kMB, NG = Cfg::kGroups, GW = Cfg::kGW;
   constexpr int kBox = Cfg::kBox;
   constexpr uint32_t O0 = Cfg::kO0, K0 = Cfg::kK0;
 
   extern __shared__ __align__(1024) uint8_t paged_smem_raw[];
-  __shared__ PagedSmem<RW> sm;
+  __shared__ PagedSmem<RW, N, NG> sm;
+  static_assert(Cfg::kSmem + sizeof(sm) <= 232448 - 1024, "shared memory budget");
   uint8_t* dsm = paged_smem_raw + ((1024u - (smem_u32(paged_smem_raw) & 1023u)) & 1023u);
   uint8_t* qsm = dsm + ST * Cfg::kVStage;
   uint8_t* psm = qsm + Cfg::kQBytes;
@@ -403,18 +420,20 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
     for (int s = 0; s < 3; ++s) {
       mbar_init(smem_u32(&sm.full[s]), kPagedConv);
       mbar_init(smem_u32(&sm.empty[s]), 1);
-      sm.vote[s] = 0;
+      sm.vote[0][s] = 0;
+      sm.vote[1][s] = 0;
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&sm.s_full[b]), 1);
-      mbar_init(smem_u32(&sm.s_free[b]), 8);  // the softmax warps
-      mbar_init(smem_u32(&sm.p_full[b]), 8);
+      mbar_init(smem_u32(&sm.s_free[b]), GW);
+      mbar_init(smem_u32(&sm.p_full[b]), GW);
       mbar_init(smem_u32(&sm.o_done[b]), 1);
+      mbar_init(smem_u32(&sm.vote_bar[b]), GW);
+      mbar_init(smem_u32(&sm.xchg_bar[b]), GW);
     }
-    mbar_init(smem_u32(&sm.q_ready), 8);
-    mbar_init(smem_u32(&sm.o_free), 8);
-    mbar_init(smem_u32(&sm.vote_bar), 8);
-    mbar_init(smem_u32(&sm.xchg_bar), 8);
+    mbar_init(smem_u32(&sm.q_ready), GW);
+    mbar_init(smem_u32(&sm.o_free), GW);  // the warps of group 0, which store the result
+    mbar_init(smem_u32(&sm.fin_bar), kPagedSoft);
     mbar_init(smem_u32(&sm.drain), 2);  // one commit from each issuer
     sm.abort = 0;
     p.seg_info[2 * range] = -1;
@@ -483,7 +502,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
         for (; cur.next(p, N, sg) && !aborted(); ++seg) {
           for (int t = sg.tile_lo; t < sg.tile_hi; ++t, ++n) {
             const int pb = n % PS, st = n % ST;
-            const bool first = t == sg.tile_lo;
+            const bool first = t - sg.tile_lo < NG;  // the group's first tile of the segment
+            const uint32_t od = tbase + O0 + (n % NG) * (MB * N);
             wait(sm.p_full[pb], n / PS, PW_PFULL);
             if (t == sg.tile_lo && seg > 0) wait(sm.o_free, seg - 1, PW_OFREE);
             if (aborted()) break;
@@ -495,7 +515,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
               const uint64_t vdesc = sdesc_sw128(v_base + st * Cfg::kVStage + 2 * mb * kBox, kBox, 1024);
 #pragma unroll
               for (int kk = 0; kk < TN / 16; ++kk)
-                umma_ss(tbase + O0 + N * mb, desc_add(vdesc, kk * 2048), desc_add(pdesc, kk * 2 * atom), id, first && kk == 0 ? 0u : 1u);
+                umma_ss(od + N * mb, desc_add(vdesc, kk * 2048), desc_add(pdesc, kk * 2 * atom), id, first && kk == 0 ? 0u : 1u);
             }
             umma_commit(smem_u32(&sm.o_done[pb]));
             umma_commit(smem_u32(&sm.empty[st]));
@@ -508,7 +528,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
       const WaitCtl dc{&zero, p.err, p.wait_limit_ns};
       mbar_wait(smem_u32(&sm.drain), 0, dc, kPagedSite + PW_DRAIN);
     }
-  } else if (warp >= 12) {
+  } else if (warp >= 4 + kPagedSoft) {
     // ================================================================== converters
     // Warp w takes 16 keys of every tile: lanes 16 (w / 4) .. + 15 of the TMEM quadrant w % 4.  Thread 4g + 2h + b has
     // key g + 8b and of it the 32-column chunks h + 2m (m = 0, 1 in every 128 columns) and the 16-byte pieces h + 2m of
@@ -516,7 +536,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
     // columns in that order, and Q is stored to match.  The next tile's loads are issued when this one is converted;
     // its rows were asked into L2 a tile earlier, and their page numbers one tile earlier still.
     constexpr int kKeys = kPagedTile / kPagedConv, kH = D / 128;
-    const int cw = warp - 12, key0 = 32 * (cw & 3) + 16 * (cw >> 2);
+    const int cw = warp - (4 + kPagedSoft), key0 = 32 * (cw & 3) + 16 * (cw >> 2);
     const int rr = (lane >> 2) + 8 * (lane & 1), hf = (lane >> 1) & 1;
     const int r = p.G * D;
     const uint8_t* pool = p.pages.pool;
@@ -524,7 +544,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
     struct Tile {
       int b, t, L, group;  // t < 0: none
     };
-    PagedCursor& walk = sm.walk[8 + cw];
+    PagedCursor& walk = sm.walk[kPagedSoft + cw];
     PagedSegment& seg = sm.conv_seg[cw];
     if (lane == 0) walk = sm.cur;
     int walk_t = 0, walk_hi = 0;
@@ -620,9 +640,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
       const uint32_t ktm = tlane + st * Cfg::kKCols;
 #pragma unroll
       for (int h = 0; h < kH; ++h) {
-        uint32_t out[32];
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
+          uint32_t out[16];
           const uint32_t s2 = __byte_perm(scale[2 * h + m], 0, pick);
           const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&s2);
           const __nv_bfloat162 o = __hmul2(s, __float2bfloat162_rn(-136.f));
@@ -631,13 +651,13 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
           for (int e = 0; e < 4; ++e) {
             const uint4 x = int4_expand(word[e], mask, magic, s, o);
             *reinterpret_cast<uint4*>(stage + at_word[e] + (2 * h + m) * kBox) = x;
-            out[16 * m + 4 * e] = x.x;
-            out[16 * m + 4 * e + 1] = x.y;
-            out[16 * m + 4 * e + 2] = x.z;
-            out[16 * m + 4 * e + 3] = x.w;
+            out[4 * e] = x.x;
+            out[4 * e + 1] = x.y;
+            out[4 * e + 2] = x.z;
+            out[4 * e + 3] = x.w;
           }
+          if (Cfg::kTS) tmem_st_16x64_x16(ktm + 64 * h + 32 * m, out);
         }
-        if (Cfg::kTS) tmem_st_16x64_x32(ktm + 64 * h, out);
       }
       {
         uint32_t out[16];
@@ -660,23 +680,25 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
     // ================================================================== softmax / epilogue (warps 2 and 3 are idle)
     const int sw = warp - 4;
     const int q4 = warp & 3;                     // TMEM lane quadrant
-    const int half = sw >> 2, rb = RW * half;    // rows rb .. rb + RW - 1 of the unit
-    const int k = q4 * 32 + lane;                // key of the tile; value column (of an M block) of O^T
-    const int rl = lane % RW;                    // this lane's row, rb + rl, after a reduction over lanes
+    const int set = sw >> 2;
+    const int grp = NG == 2 ? set >> 1 : 0;                // this warp's group
+    const int rb = RW * (NG == 2 ? set & 1 : set);         // rows rb .. rb + RW - 1 of the unit
+    const int k = q4 * 32 + lane;                          // key of the tile; value column (of an M block) of O^T
+    const int rl = lane % RW;                              // this lane's row, rb + rl, after a reduction over lanes
     const uint32_t tlane = tbase + (static_cast<uint32_t>(q4 * 32) << 16) + rb;
     int xc = 0, vc = 0;
     // every warp posts one value per row (lanes 0 .. RW - 1) and reads the posts of the four warps with its rows
     auto exchange = [&](float v, float (&all)[4]) {
       const int b = xc & 1;
       if (lane < RW) sm.red[b][sw][lane] = v;
-      warp_arrive(sm.xchg_bar);
-      wait(sm.xchg_bar, xc, PW_XCHG);
+      warp_arrive(sm.xchg_bar[grp]);
+      wait(sm.xchg_bar[grp], xc, PW_XCHG);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) all[w] = sm.red[b][4 * half + w][rl];
+      for (int w = 0; w < 4; ++w) all[w] = sm.red[b][4 * set + w][rl];
       ++xc;
     };
     auto load_q = [&](const PagedSegment& s) {
-      paged_load_q<D, N>(p, s, qsm, sw * 32 + lane, 256);
+      paged_load_q<D, N>(p, s, qsm, (sw % GW) * 32 + lane, 32 * GW);
       warp_arrive(sm.q_ready);
     };
 
@@ -685,8 +707,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
       if (__ldg(p.pages.seq_lens + b) > 0) continue;
       const size_t rows = static_cast<size_t>(p.s_q) * p.h_q;
       uint4* o = reinterpret_cast<uint4*>(p.out + b * rows * D);
-      for (size_t e = sw * 32 + lane; e < rows * D / 8; e += 256) o[e] = make_uint4(0u, 0u, 0u, 0u);
-      for (size_t e = sw * 32 + lane; e < rows; e += 256) p.lse[b * rows + e] = -INFINITY;
+      for (size_t e = sw * 32 + lane; e < rows * D / 8; e += 32 * kPagedSoft) o[e] = make_uint4(0u, 0u, 0u, 0u);
+      for (size_t e = sw * 32 + lane; e < rows; e += 32 * kPagedSoft) p.lse[b * rows + e] = -INFINITY;
     }
 
     // where this key's weights go: 2N bytes a key, 16-byte chunk c at c ^ the swizzle of that width
@@ -698,7 +720,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
     int n0 = 0, seg = 0;  // the tile count at the segment's start
     float l[RW];          // this key lane's share of each row's sum of weights
     bool have = paged_next(p, N, walk, sm.seg[sw][0], lane);
-    if (have) load_q(sm.seg[sw][0]);
+    if (have && grp == 0) load_q(sm.seg[sw][0]);
     for (; have; ++seg) {
       const PagedSegment& sg = sm.seg[sw][seg & 1];
       PagedSegment& nx = sm.seg[sw][(seg + 1) & 1];
@@ -709,9 +731,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
       float m_run = 0.f;                                    // reference of row rb + rl (log2 units)
 #pragma unroll
       for (int j = 0; j < RW; ++j) l[j] = 0.f;
-      for (int j = 0; j < tiles; ++j) {
+      const int j0 = NG == 2 ? (n0 ^ grp) & 1 : 0;
+      for (int j = j0; j < tiles; j += NG) {
         const int n = n0 + j, sb = n % SS, pb = n % PS;
-        const bool first = j == 0;
+        const bool first = j == j0;
         wait(sm.s_full[sb], n / SS, PW_SFULL);
         tc_fence_after();
         // the tile's scores, -inf where the row does not see the key
@@ -743,12 +766,12 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
           }
           // The flag of vote vc is one of three words: it is cleared after vote vc + 1, when every warp has read
           // it, and set again for vote vc + 3 by warps that passed vote vc + 2, which this warp joins after clearing.
-          volatile uint32_t* flag = sm.vote;
+          volatile uint32_t* flag = sm.vote[grp];
           if (__any_sync(0xffffffffu, top > kPagedRaise) && lane == 0) flag[vc % 3] = 1u;
-          warp_arrive(sm.vote_bar);
-          wait(sm.vote_bar, vc, PW_VOTE);
-          raise = flag[vc % 3] != 0;  // the same for all softmax warps
-          if (sw == 0 && lane == 0) flag[(vc + 2) % 3] = 0u;
+          warp_arrive(sm.vote_bar[grp]);
+          wait(sm.vote_bar[grp], vc, PW_VOTE);
+          raise = flag[vc % 3] != 0;  // the same for all the group's warps
+          if (sw % GW == 0 && lane == 0) flag[(vc + 2) % 3] = 0u;
           ++vc;
         }
         if (raise) {
@@ -762,17 +785,17 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
           float all[4];
           exchange(mw, all);
           const float mt = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
-          // a row that sees no key of the segment's first tile sees none of its later ones: its reference stays 0
+          // a row that sees no key of the group's first tile sees none of its later ones: its reference stays 0
           const float up = first ? (mt == -INFINITY ? 0.f : mt) : fmaxf(mt, 0.f);
           m_run = first ? up : m_run + up;
           if (lane < RW) {
             sm.ref[sw][lane] = m_run;
-            sm.fac[sw][lane] = up;
+            sm.fac[sw][0][lane] = up;
           }
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < RW; ++i) {
-            const float u = *const_cast<volatile float*>(&sm.fac[sw][i]);
+            const float u = *const_cast<volatile float*>(&sm.fac[sw][0][i]);
             x[i] -= u;
             l[i] = first ? 0.f : l[i] * ex2_approx(-u);
           }
@@ -785,7 +808,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
           l[2 * i + 1] += e1;
           pw[i] = pack_bf16x2(e0, e1);
         }
-        // P buffer pb was last read by PV(n - PS)
+        // P buffer pb was last read by PV(n - PS), the group's previous tile where the groups take turns
         if (n >= PS) wait(sm.o_done[pb], n / PS - 1, PW_ODONE);
         uint8_t* prow = prow0 + pb * Cfg::kPBytes;
 #pragma unroll
@@ -794,10 +817,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
               make_uint4(pw[4 * c], pw[4 * c + 1], pw[4 * c + 2], pw[4 * c + 3]);
         fence_proxy_async_smem();
         if (raise && !first) {
-          // O^T holds the segment's tiles up to the one before
-          wait(sm.o_done[(n - 1) % PS], (n - 1) / PS, PW_ODONE);
+          // O^T holds the group's tiles up to the one before
+          if (NG == 1) wait(sm.o_done[(n - 1) % PS], (n - 1) / PS, PW_ODONE);
           tc_fence_after();
-          paged_rescale<RW, N, MB>(tlane + O0, sm.fac[sw]);
+          paged_rescale<RW, N, MB>(tlane + O0 + grp * (MB * N), sm.fac[sw][0]);
         }
         tc_fence_before();
         warp_arrive(sm.p_full[pb]);
@@ -805,30 +828,50 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
       // ---------------------------------------------------------------- the segment's end
       const int n_last = n0 + tiles - 1;
       const bool have_nx = paged_next(p, N, walk, nx, lane);
-      if (have_nx) load_q(nx);  // the unit's QKs are done
+      // the group with the last tile loads Q: that tile's QK, the unit's last, is done
+      if (have_nx && grp == (NG == 2 ? n_last & 1 : 0)) load_q(nx);
       float lt[4];
       exchange(paged_rows_reduce<false, RW>(l, lane), lt);
-      const float lsum = (lt[0] + lt[1]) + (lt[2] + lt[3]);  // a NaN stays one in both results
-      __syncwarp();
-      if (lane < RW) {
-        sm.fac[sw][lane] = lsum == 0.f ? 0.f : 1.f / lsum;
-        const int g = sg.row0 + rb + lane;
-        if (q4 == 0 && g < p.R) {
-          const float lse = lsum == 0.f ? -INFINITY : (m_run + log2f(lsum)) * 0.69314718055994531f;
-          const int i = g >= p.hpg;
-          if (sg.slot < 0)
-            p.lse[(static_cast<size_t>(sg.b) * p.s_q + i) * p.h_q + sg.group * p.hpg + (g - i * p.hpg)] = lse;
-          else
-            p.part_lse[static_cast<size_t>(2 * range + sg.slot) * N + rb + lane] = lse;
-        }
+      const int f = seg & 1;
+      if (q4 == 0 && lane < RW) {
+        sm.fin_m[f][grp][rb + lane] = m_run;
+        sm.fin_l[f][grp][rb + lane] = (lt[0] + lt[1]) + (lt[2] + lt[3]);
       }
-      __syncwarp();
-      wait(sm.o_done[n_last % PS], n_last / PS, PW_ODONE);
-      tc_fence_after();
-      paged_store_out<D, N, RW>(p, sg, tlane + O0, sm.fac[sw], rb, k, static_cast<size_t>(2 * range + (sg.slot < 0 ? 0 : sg.slot)) * N);
-      if (sg.slot >= 0 && sw == 0 && lane == 0) p.seg_info[2 * range + sg.slot] = 4 * sg.unit + sg.first + 2 * sg.last;
-      tc_fence_before();
-      warp_arrive(sm.o_free);
+      warp_arrive(sm.fin_bar);
+      wait(sm.fin_bar, seg, PW_FIN);
+      if (grp == 0) {
+        // out = sum_g 2^(m_g - m) O_g / sum_g 2^(m_g - m) l_g over the groups that saw a key
+        const int row = rb + rl;
+        const float l0 = sm.fin_l[f][0][row], l1 = NG == 2 ? sm.fin_l[f][NG - 1][row] : 0.f;
+        const float m0 = l0 == 0.f ? -INFINITY : sm.fin_m[f][0][row];
+        const float m1 = l1 == 0.f ? -INFINITY : sm.fin_m[f][NG - 1][row];
+        const float m = fmaxf(m0, m1);
+        const float w0 = l0 == 0.f ? 0.f : ex2_approx(m0 - m), w1 = l1 == 0.f ? 0.f : ex2_approx(m1 - m);
+        const float sum = w0 * l0 + w1 * l1;  // a NaN stays one in both results
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        if (lane < RW) {
+          sm.fac[sw][0][lane] = w0 * inv;
+          if (NG == 2) sm.fac[sw][NG - 1][lane] = w1 * inv;
+          const int g = sg.row0 + row;
+          if (q4 == 0 && g < p.R) {
+            const float lse = sum == 0.f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994531f;
+            const int i = g >= p.hpg;
+            if (sg.slot < 0)
+              p.lse[(static_cast<size_t>(sg.b) * p.s_q + i) * p.h_q + sg.group * p.hpg + (g - i * p.hpg)] = lse;
+            else
+              p.part_lse[static_cast<size_t>(2 * range + sg.slot) * N + row] = lse;
+          }
+        }
+        __syncwarp();
+        wait(sm.o_done[n_last % PS], n_last / PS, PW_ODONE);  // the commit covers the MMAs before it too
+        tc_fence_after();
+        const int used = NG == 1 ? 1 : tiles > 1 ? 3 : 1 << (n_last & 1);
+        paged_store_out<D, N, RW>(p, sg, tlane + O0, &sm.fac[sw][0][0], used, rb, k,
+                                  static_cast<size_t>(2 * range + (sg.slot < 0 ? 0 : sg.slot)) * N);
+        if (sg.slot >= 0 && sw == 0 && lane == 0) p.seg_info[2 * range + sg.slot] = 4 * sg.unit + sg.first + 2 * sg.last;
+        tc_fence_before();
+        warp_arrive(sm.o_free);
+      }
       n0 += tiles;
       have = have_nx;
     }
