@@ -24,7 +24,6 @@ One decode step over a paged 4-bit cache (MLA absorbed: groups = 1; tokens alrea
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import math
@@ -516,39 +515,40 @@ def output_projection(o, w_o, out_dtype=torch.float32, out=None, stream=None):
 # Rotary positions and the paged 4-bit cache
 # ------------------------------------------------------------------------------------------------
 
-@functools.lru_cache(maxsize=None)
-def _sms_of(index: int) -> int:
-    return _num_sms(index)
-
-
-def _on_device(where: str, ref: torch.Tensor, **named):
-    """Every tensor given has to be on ref's GPU."""
-    if ref.device.type != "cuda":
+def _gpu_of(where: str, ref: torch.Tensor, *others) -> int:
+    """Index of ref's GPU; every other tensor given (None: not given) has to be on it too."""
+    index = ref.get_device()
+    if index < 0:
         raise ValueError(f"{where} takes tensors on a GPU")
-    for name, t in named.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{where}: {name} is on {t.device}, expected {ref.device}")
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{where}: every tensor must be on {ref.device}, got one on {t.device}")
+    return index
 
 
-def _call(where: str, device, stream, f, *args):
-    """f(*args, stream) with the tensors' device current, on its current stream unless one is given."""
-    if device.index == torch.cuda.current_device():
-        _ck(f(*args, _stream(stream)), where)
+def _call(where: str, index: int, stream, f, *args):
+    """f(*args, stream) with the tensors' GPU current, on its current stream unless one is given."""
+    if index == torch.cuda.current_device():
+        status = f(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     else:
-        with torch.cuda.device(device):
-            _ck(f(*args, _stream(stream)), where)
+        with torch.cuda.device(index):
+            status = f(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+    if status != OK:
+        raise LkvError(status, where)
 
 
-def _alloc_on(stream):
-    """Allocations for a call on `stream`: from that stream's pool, so that a workspace freed at the call's return is
-    not handed to another stream while the kernels run."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _empty_on(stream, shape, dtype, device):
+    """An uninitialised tensor for a call on `stream`: from that stream's pool, so that a workspace freed at the call's
+    return is not handed to another stream while the kernels run."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _int32(**named):
-    for name, t in named.items():
-        if t is not None and t.dtype != torch.int32:
-            raise TypeError(f"{name} is {t.dtype}, expected torch.int32")
+def _expect(t, dtype, name):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
 
 
 def rope_frequencies(rot: int, base: float = 10000.0, factor: float = 1.0, context: int = 4096,
@@ -579,20 +579,23 @@ def rope_rotate(x, positions, freqs, first=0, interleaved=False, inverse=False, 
     copied.  Pairs are columns (i, i + rot / 2) of that part, or (2i, 2i + 1) if interleaved.  inverse=True applies
     the transpose: the gradient of x from the gradient of the result.  out: a new tensor, or x itself (in place), or
     one that does not overlap x.  Returns out."""
-    _same_dtype(x, out=out)
-    _int32(positions=positions)
-    if freqs.dtype != torch.float64:
-        raise TypeError(f"freqs is {freqs.dtype}, expected torch.float64")
-    _on_device("rope_rotate", x, positions=positions, freqs=freqs, out=out)
-    if x.dim() < 3 or x.stride(-1) != 1:
+    dtype = x.dtype
+    if dtype != torch.bfloat16 and dtype != torch.float32:
+        raise TypeError(f"unsupported dtype {dtype}")
+    _expect(positions, torch.int32, "positions")
+    _expect(freqs, torch.float64, "freqs")
+    if out is not None:
+        _expect(out, dtype, "out")
+    index = _gpu_of("rope_rotate", x, positions, freqs, out)
+    shape = x.shape
+    if len(shape) < 3 or x.stride(-1) != 1:
         raise ValueError("x must be [..., heads, d] with unit inner stride")
     if out is None:
-        with _alloc_on(stream):
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape or out.stride(-1) != 1 or (out.data_ptr() == x.data_ptr() and out.stride() != x.stride()):
+        out = _empty_on(stream, shape, dtype, x.device)
+    elif out.shape != shape or out.stride(-1) != 1 or (out.data_ptr() == x.data_ptr() and out.stride() != x.stride()):
         raise ValueError("out must have x's shape and unit inner stride, and x's strides if it is x's memory")
-    heads, d = x.shape[-2:]
-    xs, os_ = (x, out) if x.dim() == 3 else (x.view(-1, heads, d), out.view(-1, heads, d))
+    heads, d = shape[-2:]
+    xs, os_ = (x, out) if len(shape) == 3 else (x.view(-1, heads, d), out.view(-1, heads, d))
     n = xs.shape[0]
     if positions.numel() != n:
         raise ValueError("positions must hold one position for each token")
@@ -600,9 +603,11 @@ def rope_rotate(x, positions, freqs, first=0, interleaved=False, inverse=False, 
         raise ValueError("freqs must be [rot / 2]; freqs and positions contiguous")
     if n == 0 and heads > 0 and d > 0:
         return out
-    _call("lkv_rope_rotate", x.device, stream, _rope, _ptr(xs), xs.stride(0), xs.stride(1), _ptr(positions), _ptr(freqs),
-          n, heads, d, int(first), 2 * freqs.numel(), int(interleaved), int(inverse), float(gain), _dtype_code(x),
-          _ptr(os_), os_.stride(0), os_.stride(1))
+    x_ts, x_hs, _ = xs.stride()
+    o_ts, o_hs, _ = os_.stride()
+    _call("lkv_rope_rotate", index, stream, _rope, x.data_ptr(), x_ts, x_hs, positions.data_ptr(), freqs.data_ptr(), n,
+          heads, d, first, 2 * freqs.numel(), interleaved, inverse, gain, BF16 if dtype == torch.bfloat16 else FP32,
+          out.data_ptr(), o_ts, o_hs)
     return out
 
 
@@ -621,20 +626,23 @@ def int4_cache_fields(pool, r: int, d_rope: int):
             pool[..., rb - 2 * d_rope:rb].view(torch.bfloat16))
 
 
-def _pool_args(where, ref, pool, block_table, seq_lens):
-    """The pool's and table's arguments of the C calls, up to seq_lens and the batch."""
+def _pool_args(where, pool, block_table, seq_lens):
+    """The pool's and table's arguments of the C calls, up to seq_lens, and the batch."""
     if pool.dtype != torch.uint8:
         raise TypeError(f"{where} takes a uint8 pool")
-    _int32(block_table=block_table, seq_lens=seq_lens)
-    _on_device(where, ref, pool=pool, block_table=block_table, seq_lens=seq_lens)
+    _expect(block_table, torch.int32, "block_table")
+    _expect(seq_lens, torch.int32, "seq_lens")
     if pool.dim() != 3 or pool.stride(2) != 1:
         raise ValueError("pool must be [pages, page_size, >= row_bytes] with contiguous rows")
     B = seq_lens.numel()
     if (block_table.dim() != 2 or block_table.shape[0] != B or block_table.stride(1) != 1 or seq_lens.dim() != 1
             or not seq_lens.is_contiguous()):
         raise ValueError("block_table must be [batch, max_pages] with contiguous rows, seq_lens [batch] contiguous")
-    return (_ptr(pool), pool.stride(0), pool.stride(1), pool.shape[0], pool.shape[1], _ptr(block_table),
-            block_table.stride(0) if B > 1 else block_table.shape[1], block_table.shape[1], _ptr(seq_lens)), B
+    pages, page_size, _ = pool.shape
+    page_stride, row_stride, _ = pool.stride()
+    columns = block_table.shape[1]
+    return (pool.data_ptr(), page_stride, row_stride, pages, page_size, block_table.data_ptr(),
+            block_table.stride(0) if B > 1 else columns, columns, seq_lens.data_ptr()), B
 
 
 def paged_append_int4(new_rows, pool, r, block_table, seq_lens, cu_new=None, freqs=None, gain=1.0, interleaved=False,
@@ -644,18 +652,20 @@ def paged_append_int4(new_rows, pool, r, block_table, seq_lens, cu_new=None, fre
     rope_frequencies; freqs=None: stored as it comes).  seq_lens [batch] int32 counts each request's tokens, the new
     ones among them; rows cu_new[b] .. cu_new[b + 1] - 1 are the newest of request b (cu_new=None: n / batch each).
     rows_out: gets the values the cache now holds (bf16, new_rows' shape; may be new_rows).  Returns pool."""
-    _same_dtype(new_rows, rows_out=rows_out)
     if new_rows.dtype != torch.bfloat16:
         raise TypeError("paged_append_int4 takes bf16 rows")
-    _int32(cu_new=cu_new)
-    if freqs is not None and freqs.dtype != torch.float64:
-        raise TypeError(f"freqs is {freqs.dtype}, expected torch.float64")
-    args, B = _pool_args("paged_append_int4", new_rows, pool, block_table, seq_lens)
-    _on_device("paged_append_int4", new_rows, cu_new=cu_new, freqs=freqs, rows_out=rows_out)
+    args, B = _pool_args("paged_append_int4", pool, block_table, seq_lens)
+    if rows_out is not None:
+        _expect(rows_out, torch.bfloat16, "rows_out")
+    if cu_new is not None:
+        _expect(cu_new, torch.int32, "cu_new")
+    if freqs is not None:
+        _expect(freqs, torch.float64, "freqs")
+    index = _gpu_of("paged_append_int4", new_rows, pool, block_table, seq_lens, cu_new, freqs, rows_out)
     if new_rows.dim() != 2:
         raise ValueError("new_rows must be [n, r + d_rope]")
     n, width = new_rows.shape
-    rb = int4_cache_row_bytes(r, width - r)
+    rb = _row_bytes_of(r, width - r)
     if rb == 0 or pool.shape[2] < rb:
         raise ValueError("unsupported r / d_rope, or pool rows shorter than int4_cache_row_bytes(r, d_rope)")
     if cu_new is not None and (cu_new.numel() != B + 1 or not cu_new.is_contiguous()):
@@ -666,14 +676,24 @@ def paged_append_int4(new_rows, pool, r, block_table, seq_lens, cu_new=None, fre
         raise ValueError("rows_out must have new_rows' shape")
     if n == 0:
         return pool
-    _call("lkv_paged_append_int4", new_rows.device, stream, _paged_append, _ptr(new_rows), _row_stride(new_rows), n,
-          *args, _ptr(cu_new), B, int(r), width - r, _ptr(freqs), int(interleaved), float(gain), _ptr(rows_out),
-          0 if rows_out is None else _row_stride(rows_out))
+    _call("lkv_paged_append_int4", index, stream, _paged_append, new_rows.data_ptr(), _row_stride(new_rows), n, *args,
+          None if cu_new is None else cu_new.data_ptr(), B, r, width - r, None if freqs is None else freqs.data_ptr(),
+          interleaved, gain, None if rows_out is None else rows_out.data_ptr(), 0 if rows_out is None else _row_stride(rows_out))
     return pool
 
 
 def paged_decode_workspace_size(batch, s_q, h_q, groups, d, num_sms) -> int:
     return _paged_ws(batch, s_q, h_q, groups, d, num_sms)
+
+
+@functools.lru_cache(maxsize=None)
+def _row_bytes_of(r: int, d_rope: int) -> int:
+    return _int4_row_bytes(r, d_rope)
+
+
+@functools.lru_cache(maxsize=None)
+def _paged_ws_on(index: int, batch, s_q, h_q, groups, d) -> int:
+    return max(_paged_ws(batch, s_q, h_q, groups, d, _num_sms(index)), 256)
 
 
 def paged_decode_int4(q, q_rope, pool, groups, block_table, seq_lens, scale, out=None, lse=None, workspace=None,
@@ -683,29 +703,30 @@ def paged_decode_int4(q, q_rope, pool, groups, block_table, seq_lens, scale, out
     row's RoPE key) and value of group j's heads: d = 128 (GTA), 256 (GLA) or 512 (MLA absorbed, groups = 1).
     block_table [B, max_pages] and seq_lens [B] int32.  Queries that see no token get out = 0, lse = -inf.
     Returns (out [B,s_q,h_q,d], lse [B,s_q,h_q] fp32)."""
-    _same_dtype(q, q_rope=q_rope, out=out)
-    if q.dtype != torch.bfloat16:
+    if q.dtype != torch.bfloat16 or q_rope.dtype != torch.bfloat16:
         raise TypeError("paged_decode_int4 takes a bf16 query")
-    args, B = _pool_args("paged_decode_int4", q, pool, block_table, seq_lens)
-    _on_device("paged_decode_int4", q, q_rope=q_rope, out=out, lse=lse, workspace=workspace)
-    if q.dim() != 4 or q.shape[0] != B or q_rope.shape[:-1] != q.shape[:-1]:
+    args, B = _pool_args("paged_decode_int4", pool, block_table, seq_lens)
+    index = _gpu_of("paged_decode_int4", q, q_rope, pool, block_table, seq_lens, out, lse, workspace)
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != B or q_rope.shape[:-1] != shape[:-1]:
         raise ValueError("q must be [batch, s_q, h_q, d] and q_rope [batch, s_q, h_q, d_rope]")
-    _, s_q, h_q, d = q.shape
+    _, s_q, h_q, d = shape
     d_r = q_rope.shape[-1]
-    rb = int4_cache_row_bytes(groups * d, d_r)
+    rb = _row_bytes_of(groups * d, d_r)
     if rb == 0 or pool.shape[2] < rb:
         raise ValueError("unsupported groups * d / d_rope, or pool rows shorter than int4_cache_row_bytes(groups * d, d_rope)")
-    with _alloc_on(stream):
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if lse is None:
-            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = _alloc_ws(_paged_ws(B, s_q, h_q, groups, d, _sms_of(q.device.index)), q.device)
-    if out.shape != q.shape or lse.shape != q.shape[:-1] or lse.dtype != torch.float32:
-        raise ValueError("out must have q's shape, lse [batch, s_q, h_q] fp32")
-    _contig(q, q_rope, out, lse, workspace)
-    _call("lkv_paged_decode_int4", q.device, stream, _paged_decode, _ptr(q), _ptr(q_rope), *args, B, s_q, h_q,
-          int(groups), d, d_r, float(scale), _ptr(out), _ptr(lse), _ptr(workspace),
-          workspace.numel() * workspace.element_size())
+    if out is None:
+        out = _empty_on(stream, shape, torch.bfloat16, q.device)
+    elif out.shape != shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
+        raise ValueError("out must be contiguous bf16 of q's shape")
+    if lse is None:
+        lse = _empty_on(stream, shape[:-1], torch.float32, q.device)
+    elif lse.shape != shape[:-1] or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous [batch, s_q, h_q] fp32")
+    if workspace is None:
+        workspace = _empty_on(stream, _paged_ws_on(index, B, s_q, h_q, groups, d), torch.uint8, q.device)
+    if not q.is_contiguous() or not q_rope.is_contiguous() or not workspace.is_contiguous():
+        raise ValueError("query and workspace tensors must be contiguous")
+    _call("lkv_paged_decode_int4", index, stream, _paged_decode, q.data_ptr(), q_rope.data_ptr(), *args, B, s_q, h_q,
+          groups, d, d_r, scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes)
     return out, lse

@@ -60,11 +60,11 @@ lkv_status check_pool(Paged* g, const void* pool, int64_t page_stride, int64_t r
 }
 
 template <typename T, int V>
-void launch_rope(const RopeParams& p, bool interleaved, unsigned blocks, cudaStream_t s) {
+void launch_rope(const RopeParams& p, bool interleaved, dim3 blocks, dim3 threads, cudaStream_t s) {
   if (interleaved)
-    rope_kernel<T, V, true><<<blocks, kRopeThreads, 0, s>>>(p);
+    rope_kernel<T, V, true><<<blocks, threads, 0, s>>>(p);
   else
-    rope_kernel<T, V, false><<<blocks, kRopeThreads, 0, s>>>(p);
+    rope_kernel<T, V, false><<<blocks, threads, 0, s>>>(p);
 }
 
 // Rows of a unit (the MMA's N): the smallest of 16, 32, 64 that holds a group's rows, so that small groups
@@ -182,30 +182,36 @@ lkv_status lkv_rope_rotate(const void* x, int64_t x_token_stride, int64_t x_head
                    (interleaved ? rot : rot / 2) % wide == 0;
   const int v = vec ? wide : 1;
   const int items = (interleaved ? rot / (vec ? wide : 2) : rot / 2 / v) + (p.copy ? (d - rot) / v : 0);
-  p.bx = items < kRopeThreads ? items : kRopeThreads;
-  p.by = kRopeThreads / p.bx;
-  const int rows = p.by * kRopeUnroll;
-  const int chunks = (heads + rows - 1) / rows;
-  p.head_block = (heads + chunks - 1) / chunks;
+  const int bx = items < kRopeThreads ? items : kRopeThreads, by = kRopeThreads / bx;
+  // A block takes one load of each thread's rows: several tokens where their heads do not fill it, else the heads of
+  // one token, more of them at a time (up to 4 such loads for one table) the more blocks there are.
+  const int rows = by * kRopeUnroll;
   p.tok_block = 1;
-  if (chunks == 1) {
+  p.head_block = heads;
+  if (heads <= rows) {
     const int most = kRopeTable / (rot / 2);
     p.tok_block = rows / heads < most ? rows / heads : most;
+  } else {
+    int loads = 4;
+    while (loads > 1 && n_tok * ((heads + loads * rows - 1) / (loads * rows)) < 2048) --loads;
+    const int chunks = (heads + loads * rows - 1) / (loads * rows);
+    p.head_block = (heads + chunks - 1) / chunks;
   }
-  const int64_t blocks = (n_tok + p.tok_block - 1) / p.tok_block * ((heads + p.head_block - 1) / p.head_block);
-  if (blocks > INT_MAX) return LKV_ERR_UNSUPPORTED;
-  const unsigned nb = static_cast<unsigned>(blocks);
+  const int64_t nx = (n_tok + p.tok_block - 1) / p.tok_block;
+  const int ny = (heads + p.head_block - 1) / p.head_block;
+  if (nx > INT_MAX || ny > 65535) return LKV_ERR_UNSUPPORTED;
+  const dim3 blocks(static_cast<unsigned>(nx), ny), threads(bx, by);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == LKV_BF16) {
     if (vec)
-      launch_rope<__nv_bfloat16, 8>(p, interleaved, nb, s);
+      launch_rope<__nv_bfloat16, 8>(p, interleaved, blocks, threads, s);
     else
-      launch_rope<__nv_bfloat16, 1>(p, interleaved, nb, s);
+      launch_rope<__nv_bfloat16, 1>(p, interleaved, blocks, threads, s);
   } else {
     if (vec)
-      launch_rope<float, 4>(p, interleaved, nb, s);
+      launch_rope<float, 4>(p, interleaved, blocks, threads, s);
     else
-      launch_rope<float, 1>(p, interleaved, nb, s);
+      launch_rope<float, 1>(p, interleaved, blocks, threads, s);
   }
   return launched();
 }

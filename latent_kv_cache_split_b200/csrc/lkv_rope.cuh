@@ -31,13 +31,12 @@ struct RopeParams {
   int heads, d, first, rot;
   int inverse, copy;  // copy: the columns outside the rotated part go to `out` too
   float gain;
-  int bx, by;      // threads: bx along a head's items, by along (token, head) rows
   int tok_block;   // tokens of a block
-  int head_block;  // heads of a block (tok_block is 1 where this is less than all)
+  int head_block;  // heads of a block (all of them where tok_block > 1)
 };
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeUnroll = 4;  // (token, head) rows of a thread, all loaded before any is used
+constexpr int kRopeUnroll = 4;  // (token, head) rows of a thread that are loaded before any is used
 constexpr int kRopeMaxPairs = 512;
 constexpr int kRopeTable = 2048;  // (cos, sin) entries of a block: 16 KB
 
@@ -59,12 +58,13 @@ struct alignas(sizeof(T) * V) RopeVec {
   T v[V];
 };
 
-// One item is V columns of the half layout's lower half with their partners, 2 columns or V of the
-// interleaved layout, or V copied columns.  Every element is read and written once, by one thread, so
-// x and out may be the same array.  The kernel is bound by memory: a block's (cos, sin) table costs one
-// fp64 angle a pair and is shared by its heads, and its loads are issued before the table is built.
+// Threads x run along a head's items, threads y along the block's (token, head) rows.  An item is V columns of the half
+// layout's lower half with their partners, 2 columns or V of the interleaved layout, or V copied columns.  Every element
+// is read and written once, by one thread, so x and out may be the same array.  The kernel is bound by memory: a block's
+// (cos, sin) table costs one fp64 angle a pair and is shared by its heads, and its first loads are issued before the
+// table is built.
 template <typename T, int V, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
   __shared__ float2 table[kRopeTable];
   constexpr int kIV = kInterleaved && V == 1 ? 2 : V;  // columns of an interleaved item
   using Vec = RopeVec<T, V>;
@@ -72,20 +72,18 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   const int rot_items = kInterleaved ? p.rot / kIV : half / V;
   const int left = p.first / V;  // copied items before the rotated part
   const int items = rot_items + (p.copy ? (p.d - p.rot) / V : 0);
-  const int tid = threadIdx.x;
-  const int tx = tid % p.bx, ty = tid / p.bx;
-  const int head_chunks = (p.heads + p.head_block - 1) / p.head_block;
-  const long long tok0 = static_cast<long long>(blockIdx.x / head_chunks) * p.tok_block;
-  const int h0 = (blockIdx.x % head_chunks) * p.head_block;
+  const int ty = threadIdx.y, by = blockDim.y, tid = ty * blockDim.x + threadIdx.x;
+  const int h0 = blockIdx.y * p.head_block;
+  const long long tok0 = static_cast<long long>(blockIdx.x) * p.tok_block;
   const int nh = min(p.head_block, p.heads - h0);
   const int nt = static_cast<int>(min(static_cast<long long>(p.tok_block), p.n_tok - tok0));
   const int rows = nt * nh;
-  const T* x = static_cast<const T*>(p.x);
-  T* out = static_cast<T*>(p.out);
-  bool first_pass = true;
-  for (int it0 = 0; it0 < items; it0 += p.bx) {
-    const int it = it0 + tx;
-    const bool live = it < items && ty < p.by;
+  const T* x = static_cast<const T*>(p.x) + tok0 * p.x_ts + h0 * p.x_hs;
+  T* out = static_cast<T*>(p.out) + tok0 * p.o_ts + h0 * p.o_hs;
+  bool fresh = true;  // the table is still to be built
+  for (int it0 = 0; it0 < items; it0 += blockDim.x) {
+    const int it = it0 + threadIdx.x;
+    const bool live = it < items;
     // columns of this item: c0 (and c1, its partners in the half layout)
     int c0, c1 = 0, pair0 = -1;
     if (it < rot_items) {
@@ -97,37 +95,36 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
       c0 = k < left ? k * V : p.rot + k * V;
     }
     const bool two = pair0 >= 0 && (!kInterleaved || V == 1);
-    for (int r0 = 0; r0 < rows; r0 += p.by * kRopeUnroll) {
+    for (int r0 = ty; r0 - ty < rows; r0 += by * kRopeUnroll) {
       Vec a[kRopeUnroll], b[kRopeUnroll];
-      int tok[kRopeUnroll], head[kRopeUnroll];
 #pragma unroll
       for (int u = 0; u < kRopeUnroll; ++u) {
-        const int r = r0 + u * p.by + ty;
-        tok[u] = -1;
+        const int r = r0 + u * by;
         if (live && r < rows) {
-          tok[u] = r / nh;
-          head[u] = h0 + r - tok[u] * nh;
-          const T* row = x + (tok0 + tok[u]) * p.x_ts + head[u] * p.x_hs;
+          const int t = nt == 1 ? 0 : r / nh;
+          const T* row = x + t * p.x_ts + (r - t * nh) * p.x_hs;
           a[u] = *reinterpret_cast<const Vec*>(row + c0);
           if (two) b[u] = *reinterpret_cast<const Vec*>(row + c1);
         }
       }
-      if (first_pass) {
-        for (int e = tid; e < nt * half; e += kRopeThreads) {
-          const int t = e / half;
+      if (fresh) {  // the first pass of every thread
+        for (int e = tid; e < nt * half; e += blockDim.x * by) {
+          const int t = nt == 1 ? 0 : e / half;
           float2 cs = rope_cos_sin(p.pos[tok0 + t], p.freqs[e - t * half], p.gain);
           if (p.inverse) cs.y = -cs.y;
           table[e] = cs;
         }
         __syncthreads();
-        first_pass = false;
+        fresh = false;
       }
 #pragma unroll
       for (int u = 0; u < kRopeUnroll; ++u) {
-        if (tok[u] < 0) continue;
-        T* row = out + (tok0 + tok[u]) * p.o_ts + head[u] * p.o_hs;
+        const int r = r0 + u * by;
+        if (!live || r >= rows) continue;
+        const int t = nt == 1 ? 0 : r / nh;
+        T* row = out + t * p.o_ts + (r - t * nh) * p.o_hs;
         if (pair0 >= 0) {
-          const float2* cs = table + tok[u] * half + pair0;
+          const float2* cs = table + t * half + pair0;
           if (two) {
 #pragma unroll
             for (int k = 0; k < V; ++k) {
