@@ -63,18 +63,28 @@ struct AppendParams {
 
 constexpr int kAppendThreads = 256;
 
-// Request of new row w: the last b with cu[b] <= w.  One step looks at 32 places of the range at once.
-__device__ __forceinline__ int request_of(const int* cu, int batch, long long w, int lane) {
+// Request of new row w: the last b with cu[b] <= w, its rows [begin, end) and its token count.  One step looks at 32
+// places of the range at once, and the last one brings the request's own numbers with it, so that a batch of up to 32
+// costs one load's latency.
+__device__ __forceinline__ int request_of(const int* cu, const int* seq_lens, int batch, long long w, int lane, int& begin, int& end,
+                                          int& len) {
   int lo = 0, hi = batch;  // cu[lo] <= w < cu[hi]
-  while (hi - lo > 1) {
+  while (true) {
     const int step = (hi - lo + 31) / 32;
     const int at = lo + lane * step;
-    const unsigned below = __ballot_sync(0xffffffffu, at < hi && __ldg(cu + at) <= w);
+    const int c = at < hi ? __ldg(cu + at) : 0, l = step == 1 && at < hi ? __ldg(seq_lens + at) : 0;
+    const int next = step == 1 && at < hi ? __ldg(cu + at + 1) : 0;
+    const unsigned below = __ballot_sync(0xffffffffu, at < hi && c <= w);
     const int k = below ? 31 - __clz(below) : 0;
+    if (step == 1) {
+      begin = __shfl_sync(0xffffffffu, c, k);
+      end = __shfl_sync(0xffffffffu, next, k);
+      len = __shfl_sync(0xffffffffu, l, k);
+      return lo + k;
+    }
     lo += k * step;
     hi = min(hi, lo + step);
   }
-  return lo;
 }
 
 // One warp a row: lane l takes columns 8 (l + 32 k) .. + 7, so 4 lanes share a scale and every load and
@@ -98,12 +108,27 @@ __global__ void __launch_bounds__(kAppendThreads) append_int4_kernel(const Appen
     const int c = lane + 32 * k;
     v[k] = c < chunks ? reinterpret_cast<const uint4*>(src)[c] : make_uint4(0u, 0u, 0u, 0u);
   }
+  // the first pair of the RoPE key, ahead of the chain of loads that finds the row's place
+  const int half = p.d_rope / 2;
+  auto pair_at = [&](int i, int& c0, int& c1) {
+    c0 = p.interleaved ? 2 * i : i;
+    c1 = p.interleaved ? 2 * i + 1 : i + half;
+  };
+  __nv_bfloat16 ka = __float2bfloat16_rn(0.f), kb = ka;
+  double freq = 0.;
+  if (lane < half) {
+    int c0, c1;
+    pair_at(lane, c0, c1);
+    ka = src[p.r + c0];
+    kb = src[p.r + c1];
+    if (p.freqs) freq = __ldg(p.freqs + lane);
+  }
   int b, pos;
   if (p.cu_new) {
-    b = request_of(p.cu_new, p.batch, w, lane);
-    const int end = __ldg(p.cu_new + b + 1);
-    if (w < __ldg(p.cu_new + b) || w >= end) return;  // behind the last request's rows
-    pos = __ldg(p.pages.seq_lens + b) - (end - static_cast<int>(w));
+    int begin, end, len;
+    b = request_of(p.cu_new, p.pages.seq_lens, p.batch, w, lane, begin, end, len);
+    if (w < begin || w >= end) return;  // behind the last request's rows
+    pos = len - (end - static_cast<int>(w));
   } else {
     b = static_cast<int>(w / p.per);
     pos = __ldg(p.pages.seq_lens + b) - p.per + static_cast<int>(w - static_cast<long long>(b) * p.per);
@@ -157,12 +182,17 @@ __global__ void __launch_bounds__(kAppendThreads) append_int4_kernel(const Appen
   for (int c = p.r / kInt4Block + lane; c < int4_scale_bytes(p.r) / 2; c += 32)
     reinterpret_cast<uint16_t*>(dst + p.r / 2)[c] = 0;
   __nv_bfloat16* kd = reinterpret_cast<__nv_bfloat16*>(dst + int4_rope_at(p.r));
-  const int half = p.d_rope / 2;
   for (int i = lane; i < half; i += 32) {
-    const int c0 = p.interleaved ? 2 * i : i, c1 = p.interleaved ? 2 * i + 1 : i + half;
-    __nv_bfloat16 a = src[p.r + c0], bb = src[p.r + c1];
+    int c0, c1;
+    pair_at(i, c0, c1);
+    __nv_bfloat16 a = ka, bb = kb;
+    if (i >= 32) {
+      a = src[p.r + c0];
+      bb = src[p.r + c1];
+      if (p.freqs) freq = __ldg(p.freqs + i);
+    }
     if (p.freqs) {
-      const float2 cs = rope_cos_sin(pos, __ldg(p.freqs + i), p.gain);
+      const float2 cs = rope_cos_sin(pos, freq, p.gain);
       const float fa = __bfloat162float(a), fb = __bfloat162float(bb);
       a = __float2bfloat16_rn(fa * cs.x - fb * cs.y);
       bb = __float2bfloat16_rn(fa * cs.y + fb * cs.x);

@@ -183,18 +183,17 @@ lkv_status lkv_rope_rotate(const void* x, int64_t x_token_stride, int64_t x_head
   const int v = vec ? wide : 1;
   const int items = (interleaved ? rot / (vec ? wide : 2) : rot / 2 / v) + (p.copy ? (d - rot) / v : 0);
   const int bx = items < kRopeThreads ? items : kRopeThreads, by = kRopeThreads / bx;
-  // A block takes one load of each thread's rows: several tokens where their heads do not fill it, else the heads of
-  // one token, more of them at a time (up to 4 such loads for one table) the more blocks there are.
-  const int rows = by * kRopeUnroll;
+  // A block takes several tokens where one token's heads do not fill it, else the heads of one token: up to 16 for each
+  // row of threads, fewer where that leaves less than 2048 blocks.
   p.tok_block = 1;
   p.head_block = heads;
-  if (heads <= rows) {
+  if (heads <= by) {
     const int most = kRopeTable / (rot / 2);
-    p.tok_block = rows / heads < most ? rows / heads : most;
+    p.tok_block = by / heads < most ? by / heads : most;
   } else {
-    int loads = 4;
-    while (loads > 1 && n_tok * ((heads + loads * rows - 1) / (loads * rows)) < 2048) --loads;
-    const int chunks = (heads + loads * rows - 1) / (loads * rows);
+    int loads = 16;
+    while (loads > 1 && n_tok * ((heads + loads * by - 1) / (loads * by)) < 2048) --loads;
+    const int chunks = (heads + loads * by - 1) / (loads * by);
     p.head_block = (heads + chunks - 1) / chunks;
   }
   const int64_t nx = (n_tok + p.tok_block - 1) / p.tok_block;
