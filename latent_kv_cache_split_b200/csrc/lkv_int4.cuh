@@ -45,6 +45,20 @@ __device__ __forceinline__ long long paged_row(const Paged& g, int b, int t) {
   return page * g.page_stride + static_cast<long long>(t - k * g.page_size) * g.row_stride;
 }
 
+// Eight codes times their scale: bf16 pairs of columns (2i, 2i + 1).  mask and magic are 0x000f000f and 0x43004300
+// in registers, so that one lop3 takes both.
+__device__ __forceinline__ uint4 int4_expand(uint32_t w, uint32_t mask, uint32_t magic, __nv_bfloat162 s, __nv_bfloat162 off) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t u;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(u) : "r"(w >> (4 * i)), "r"(mask), "r"(magic));
+    __nv_bfloat162 v = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&u), s, off);
+    o[i] = *reinterpret_cast<uint32_t*>(&v);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 struct AppendParams {
   Paged pages;
   const __nv_bfloat16* rows;  // [n_new, r + d_rope]
@@ -163,19 +177,20 @@ __global__ void __launch_bounds__(kAppendThreads) append_int4_kernel(const Appen
     const int n = low ? (m + 13) / 14 : (m + 27) / 28;
     const float s = e >= 27 ? static_cast<float>(n) * __uint_as_float(static_cast<uint32_t>(e - (low ? 6 : 5)) << 23) : 0.f;
     const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-    uint32_t code = 0;
-    uint32_t back[4];
+    uint32_t code = 0u - (0x4b400000u + (0x4b400000u << 4) + (0x4b400000u << 8));  // the sums' patterns above their low bits
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float f0 = fmaf(x[2 * i], inv, 1536.f) + (12582920.f - 1536.f);
       const float f1 = fmaf(x[2 * i + 1], inv, 1536.f) + (12582920.f - 1536.f);
-      code |= ((__float_as_uint(f0) & 15u) << (4 * i)) | ((__float_as_uint(f1) & 15u) << (4 * i + 16));
-      back[i] = pack_bf16x2((f0 - 12582920.f) * s, (f1 - 12582920.f) * s);
+      code += (__float_as_uint(f0) << (4 * i)) + (__float_as_uint(f1) << (4 * i + 16));
     }
     if (c < chunks) {
       reinterpret_cast<uint32_t*>(dst)[c] = code;
       if ((lane & 3) == 0) reinterpret_cast<__nv_bfloat16*>(dst + p.r / 2)[c / 4] = __float2bfloat16_rn(s);
-      if (held) reinterpret_cast<uint4*>(held)[c] = make_uint4(back[0], back[1], back[2], back[3]);
+      if (held) {
+        const __nv_bfloat162 s2 = __float2bfloat162_rn(s);
+        reinterpret_cast<uint4*>(held)[c] = int4_expand(code, 0x000f000fu, 0x43004300u, s2, __hmul2(s2, __float2bfloat162_rn(-136.f)));
+      }
     }
   }
   // the padding of the scales' field

@@ -8,7 +8,6 @@
 #include "../../include/lkv.h"
 #include "lkv_int4.cuh"
 #include "lkv_paged_decode.cuh"
-#include "lkv_paged_warp.cuh"
 #include "lkv_rope.cuh"
 
 lkv_status lkv_internal_device_info(int** err, int* num_sms, unsigned long long* wait_ns);  // lkv_api.cu
@@ -69,7 +68,7 @@ void launch_rope(const RopeParams& p, bool interleaved, dim3 blocks, dim3 thread
 
 // Rows of a unit (the MMA's N): the smallest of 16, 32, 64 that holds a group's rows, so that small groups
 // spend no softmax on padding; 64 at most, and a group of more rows is several units that read the same tiles.
-int paged_rows(int R, int d) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }
+int paged_rows(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }
 
 struct PagedPlan {
   int N, RB, U, P, lockstep;
@@ -78,7 +77,7 @@ struct PagedPlan {
 
 void paged_plan(PagedPlan* w, int s_q, int h_q, int groups, int d, int num_sms) {
   const int R = s_q * (h_q / groups);
-  w->N = paged_rows(R, d);
+  w->N = paged_rows(R);
   w->RB = (R + w->N - 1) / w->N;
   w->U = groups * w->RB;
   // Units in lockstep share a request's RoPE keys and scales through L2; not where that leaves more than a
@@ -116,13 +115,8 @@ template <int D, int N>
 lkv_status launch_decode(const PagedDecodeParams& p, cudaStream_t s) {
   static bool ready[kMaxDevices];
   lkv_status st;
-  if constexpr (N == 1234 && D <= 256) {
-    if ((st = allow_smem(paged_warp_kernel<D>, WarpCfg<D>::kSmem, ready)) != LKV_OK) return st;
-    paged_warp_kernel<D><<<p.P, kWarpThreads, WarpCfg<D>::kSmem, s>>>(p);
-  } else {
-    if ((st = allow_smem(paged_decode_kernel<D, N>, PagedCfg<D, N>::kSmem, ready)) != LKV_OK) return st;
-    paged_decode_kernel<D, N><<<p.P, kPagedThreads, PagedCfg<D, N>::kSmem, s>>>(p);
-  }
+  if ((st = allow_smem(paged_decode_kernel<D, N>, PagedCfg<D, N>::kSmem, ready)) != LKV_OK) return st;
+  paged_decode_kernel<D, N><<<p.P, kPagedThreads, PagedCfg<D, N>::kSmem, s>>>(p);
   if ((st = launched()) != LKV_OK) return st;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.P, (N + kPagedCombineWarps - 1) / kPagedCombineWarps);

@@ -301,20 +301,6 @@ __device__ __forceinline__ void static_for(F&& f) {
   static_for_of(f, std::make_integer_sequence<int, kN>{});
 }
 
-// Eight codes times their scale: bf16 pairs of columns (2i, 2i + 1).  mask and magic are 0x000f000f and 0x43004300
-// in registers, so that one lop3 takes both.
-__device__ __forceinline__ uint4 int4_expand(uint32_t w, uint32_t mask, uint32_t magic, __nv_bfloat162 s, __nv_bfloat162 off) {
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t u;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(u) : "r"(w >> (4 * i)), "r"(mask), "r"(magic));
-    __nv_bfloat162 v = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&u), s, off);
-    o[i] = *reinterpret_cast<uint32_t*>(&v);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
 // ------------------------------------------------------------------------------------------
 // The softmax warps' rare work, out of line: inlined, its registers spilled the loop's over every tile (a spill's
 // reload misses an L1 that streams codes, and cost the loop more than half of its time).
