@@ -9,6 +9,7 @@
 #include "lkv_int4.cuh"
 #include "lkv_paged_decode.cuh"
 #include "lkv_rope.cuh"
+#include "lkv_tma_host.h"
 
 lkv_status lkv_internal_device_info(int** err, int* num_sms, unsigned long long* wait_ns);  // lkv_api.cu
 
@@ -116,7 +117,18 @@ lkv_status launch_decode(const PagedDecodeParams& p, cudaStream_t s) {
   static bool ready[kMaxDevices];
   lkv_status st;
   if ((st = allow_smem(paged_decode_kernel<D, N>, PagedCfg<D, N>::kSmem, ready)) != LKV_OK) return st;
-  paged_decode_kernel<D, N><<<p.P, kPagedThreads, PagedCfg<D, N>::kSmem, s>>>(p);
+  PagedMaps maps = {};
+  if (PagedCfg<D, N>::kTma) {
+    const Paged& g = p.pages;
+    const uint64_t rb = row_bytes_of(p.G * D, 64), ps = g.n_pages > 1 ? g.page_stride : g.row_stride * g.page_size;
+    auto map = [&](CUtensorMap* m, uint32_t bytes, CUtensorMapSwizzle sw) {
+      return make_tmap_u8_3d(m, g.pool, rb, g.page_size, g.n_pages, g.row_stride, ps, bytes, p.box_rows, sw);
+    };
+    if (!map(&maps.codes, D / 2, CU_TENSOR_MAP_SWIZZLE_NONE) || !map(&maps.scales, 16, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !map(&maps.keys, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+      return LKV_ERR_UNSUPPORTED;  // strides past what a tensor map holds
+  }
+  paged_decode_kernel<D, N><<<p.P, kPagedThreads, PagedCfg<D, N>::kSmem, s>>>(p, maps);
   if ((st = launched()) != LKV_OK) return st;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.P, (N + kPagedCombineWarps - 1) / kPagedCombineWarps);
@@ -293,6 +305,8 @@ lkv_status lkv_paged_decode_int4(const void* q, const void* q_rope, const void* 
   p.P = w.P;
   p.lockstep = w.lockstep;
   p.sl2 = scale * 1.4426950408889634f;
+  p.box_rows = page_size % 8 ? 1 : 8;
+  while (p.box_rows > 1 && p.box_rows < kPagedTile && page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   p.seg_info = reinterpret_cast<int*>(ws + w.seg);

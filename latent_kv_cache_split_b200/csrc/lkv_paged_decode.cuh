@@ -54,6 +54,13 @@ struct PagedDecodeParams {
   float* part_o;       // [2P][N][D]
   int* err;
   unsigned long long wait_limit_ns;
+  int box_rows;  // rows of a copy: the largest power of two in the page size up to 128, or 1 where that is below 8
+};
+
+// The pool as three-dimensional tensors of bytes {row, page_size, n_pages} for the copies of a group's codes, of 16 bytes
+// of scales and of the RoPE key (128-byte swizzle), box_rows rows each.
+struct PagedMaps {
+  CUtensorMap codes, scales, keys;
 };
 
 // ------------------------------------------------------------------------------------------
@@ -158,10 +165,19 @@ struct PagedCfg {
   static constexpr int kVStage = kVBoxes * kBox;  // the state in shared memory: the value operand
   // QK takes the state from TMEM where that has the columns (an MMA with both operands in shared memory reads 4 KB of
   // A there, 32 cycles of its bandwidth; from TMEM it runs at the tensor core's rate, 16 cycles at N = 32), else from
-  // the value operand's tile; the RoPE key from TMEM always.
+  // the value operand's tile.
   static constexpr bool kTS = D <= 256;
-  static constexpr int kKCols = (kTS ? D / 2 : 0) + 32;  // TMEM columns of a stage: the key operand
+  // Codes, scales and RoPE keys come by TMA into a ring of raw tiles where shared memory has the room; at D = 512 the
+  // converters load them themselves.
+  static constexpr bool kTma = D <= 256;
+  // QK reads the RoPE key from the raw tile (the copy leaves it as an MMA wants it) where the ring is deep enough to hold
+  // the tile that long, else the converters put it into TMEM.
+  static constexpr bool kKeyRaw = D == 128;
+  static constexpr int kKCols = (kTS ? D / 2 : 0) + (kKeyRaw ? 0 : 32);  // TMEM columns of a stage: the key operand
   static constexpr int kStages = D == 128 ? 3 : D == 256 ? 2 : 1;
+  static constexpr int kRaws = !kTma ? 1 : D == 256 ? (N == 16 ? 2 : 1) : N == 64 ? 2 : 3;  // raw tiles
+  static constexpr int kCodeBytes = kPagedTile * (D / 2), kScaleBytes = kPagedTile * 16;
+  static constexpr int kRawBytes = kTma ? kBox + kCodeBytes + kScaleBytes : 0;  // RoPE keys, codes, scales
   // Softmax: sets of four warps, one for each TMEM lane quadrant, with kRW rows each; at N <= 32 two groups of two sets
   // take turns at the tiles, each with accumulators, references and sums of its own, joined at the segment's end (a
   // group is bound by the latency of its chain of instructions, not by their number).
@@ -169,7 +185,7 @@ struct PagedCfg {
   static constexpr int kGW = kPagedSoft / kGroups;  // warps of a group
   static constexpr int kRW = 4 * N / kGW;           // rows of a softmax warp
   static constexpr int kSBufs = D == 256 && N == 64 ? 1 : 2;  // S^T buffers
-  static constexpr int kPs = D == 512 && N == 64 ? 1 : 2;     // P buffers
+  static constexpr int kPs = D >= 256 && N == 64 ? 1 : 2;     // P buffers
   static constexpr int kQBox = N * 128;
   static constexpr int kQBytes = (kVBoxes + 1) * kQBox;
   static constexpr int kPBytes = kPagedTile * N * 2;
@@ -177,16 +193,17 @@ struct PagedCfg {
   static constexpr uint32_t kO0 = kSBufs * N, kK0 = (kO0 + kGroups * kMB * N + 31) / 32 * 32;  // TMEM: S^T buffers, O^T, key stages
   static constexpr int kTmemNeed = kK0 + kStages * kKCols;
   static constexpr int kTmemCols = kTmemNeed <= 128 ? 128 : kTmemNeed <= 256 ? 256 : 512;
-  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kVStage + kQBytes + kPs * kPBytes;
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages) * kVStage + static_cast<size_t>(kRaws) * kRawBytes + kQBytes + kPs * kPBytes;
   static_assert(kTmemNeed <= 512, "TMEM budget");
 };
 
 constexpr int kPagedSite = LKV_SITE_WAIT_BASE + 300;  // wait sites of this kernel
-enum PagedWaitSite { PW_EMPTY = 1, PW_FULL, PW_SFREE, PW_QREADY, PW_PFULL, PW_OFREE, PW_SFULL, PW_ODONE, PW_VOTE, PW_XCHG, PW_FIN, PW_DRAIN };
+enum PagedWaitSite { PW_EMPTY = 1, PW_RAW, PW_RAWFREE, PW_FULL, PW_SFREE, PW_QREADY, PW_PFULL, PW_OFREE, PW_SFULL, PW_ODONE, PW_VOTE, PW_XCHG, PW_FIN, PW_DRAIN };
 
-template <int RW, int N, int NG>
+template <int RW, int N, int NG, int NC, int ST, int RD>
 struct __align__(16) PagedSmem {
-  uint64_t full[3], empty[3];
+  uint64_t full[ST], empty[ST];
+  uint64_t raw_full[RD], raw_free[RD];
   uint64_t s_full[2], s_free[2], p_full[2], o_done[2];
   uint64_t vote_bar[2], xchg_bar[2];  // of a softmax group
   uint64_t q_ready, o_free, fin_bar, drain;
@@ -195,11 +212,16 @@ struct __align__(16) PagedSmem {
   alignas(16) float fin_m[2][NG][N], fin_l[2][NG][N];  // [segment parity][group][row]: reference and sum at the segment's end
   alignas(16) float fac[kPagedSoft][NG][RW];  // per softmax warp: what the references rose by; then the groups' factors
   uint32_t vote[2][3];
+  alignas(16) uint8_t state[RD][kPagedTile];  // of a raw tile's keys: PagedKeyState
   uint32_t tmem_base, abort;
   // Walk state of the warps that run out of registers first: read where it is needed.
-  PagedCursor cur, walk[kPagedSoft + kPagedConv];
-  PagedSegment seg[kPagedSoft][2], conv_seg[kPagedConv];
+  PagedCursor cur, walk[kPagedSoft + NC];  // NC: the converters, or the warp that copies for them
+  PagedSegment seg[kPagedSoft][2], conv_seg[NC];
 };
+
+// A key of a raw tile: a row that was copied, a token without a page, or behind the request's end; with the group's lowest
+// bit above, which says where in the 16 bytes of scales the group's are.
+enum PagedKeyState { PK_ROW = 0, PK_NO_PAGE = 1, PK_END = 2, PK_ODD_GROUP = 4 };
 
 // The next segment of a warp's own walk, both in shared memory; the same answer in every lane.
 __device__ __noinline__ bool paged_next(const PagedDecodeParams& p, int rows, PagedCursor& walk, PagedSegment& out, int lane) {
@@ -320,7 +342,9 @@ __device__ __noinline__ void paged_load_q(const PagedDecodeParams& p, const Page
       const int i = g >= p.hpg;
       const size_t qrow = (static_cast<size_t>(s.b) * p.s_q + i) * p.h_q + s.group * p.hpg + (g - i * p.hpg);
       const __nv_bfloat16* q = p.q + qrow * D;
-      if (piece >= D / 8) {
+      if (piece >= D / 8 && PagedCfg<D, N>::kKeyRaw) {
+        x = __ldg(reinterpret_cast<const uint4*>(p.q_rope + qrow * 64) + cc);
+      } else if (piece >= D / 8) {
         const uint32_t* k = reinterpret_cast<const uint32_t*>(p.q_rope + qrow * 64) + 8 * (cc >> 1) + 2 * (cc & 1);
         x = make_uint4(__ldg(k), __ldg(k + 4), __ldg(k + 1), __ldg(k + 5));
       } else if (PagedCfg<D, N>::kTS) {
@@ -385,7 +409,8 @@ __device__ __noinline__ void paged_store_out(const PagedDecodeParams& p, const P
 }
 
 template <int D, int N>
-__global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
+__global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __grid_constant__ PagedDecodeParams p,
+                                                                           const __grid_constant__ PagedMaps maps) {
   using Cfg = PagedCfg<D, N>;
   constexpr int TN = kPagedTile, ST = Cfg::kStages, SS = Cfg::kSBufs, PS = Cfg::kPs;
   constexpr int RW = Cfg::kRW, MB = Cfg::kMB, NG = Cfg::kGroups, GW = Cfg::kGW;
@@ -393,22 +418,27 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
   constexpr uint32_t O0 = Cfg::kO0, K0 = Cfg::kK0;
 
   extern __shared__ __align__(1024) uint8_t paged_smem_raw[];
-  __shared__ PagedSmem<RW, N, NG> sm;
-  static_assert(Cfg::kSmem + sizeof(sm) <= 232448 - 1024, "shared memory budget");
+  constexpr int RD = Cfg::kRaws;
+  __shared__ PagedSmem<RW, N, NG, Cfg::kTma ? 1 : kPagedConv, ST, RD> sm;
+  static_assert(Cfg::kSmem + sizeof(sm) <= 232448, "shared memory budget");
   uint8_t* dsm = paged_smem_raw + ((1024u - (smem_u32(paged_smem_raw) & 1023u)) & 1023u);
-  uint8_t* qsm = dsm + ST * Cfg::kVStage;
+  uint8_t* raw = dsm + ST * Cfg::kVStage;
+  uint8_t* qsm = raw + RD * Cfg::kRawBytes;
   uint8_t* psm = qsm + Cfg::kQBytes;
-  const uint32_t v_base = smem_u32(dsm), q_base = smem_u32(qsm), p_base = smem_u32(psm);
+  const uint32_t v_base = smem_u32(dsm), raw_base = smem_u32(raw), q_base = smem_u32(qsm), p_base = smem_u32(psm);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int range = blockIdx.x;
 
   if (tid == 0) {
-    for (int s = 0; s < 3; ++s) {
+    for (int s = 0; s < ST; ++s) {
       mbar_init(smem_u32(&sm.full[s]), kPagedConv);
       mbar_init(smem_u32(&sm.empty[s]), 1);
-      sm.vote[0][s] = 0;
-      sm.vote[1][s] = 0;
     }
+    for (int s = 0; s < RD; ++s) {
+      mbar_init(smem_u32(&sm.raw_full[s]), 1);
+      mbar_init(smem_u32(&sm.raw_free[s]), kPagedConv + Cfg::kKeyRaw);  // the converters' reads, and QK
+    }
+    for (int s = 0; s < 3; ++s) sm.vote[0][s] = sm.vote[1][s] = 0;
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&sm.s_full[b]), 1);
       mbar_init(smem_u32(&sm.s_free[b]), GW);
@@ -456,7 +486,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
       int n = 0, seg = 0;
       auto aborted = [&] { return *const_cast<volatile uint32_t*>(&sm.abort) != 0; };
       if (warp == 0) {
-        // A = the key tile (state and RoPE key in TMEM; for D = 512 the state in shared memory), B = Q, K-major
+        // A = the key tile (the state in TMEM or, for D = 512, in shared memory, the RoPE key the other way about), B = Q
         const uint32_t id = idesc_bf16(128, N, 0, 0);
         const uint64_t qdesc = sdesc_sw128(q_base, 16, 1024);
         for (; cur.next(p, N, sg) && !aborted(); ++seg) {
@@ -469,14 +499,24 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
             tc_fence_after();
             const uint32_t ktm = tbase + K0 + st * Cfg::kKCols;
             const uint64_t kdesc = sdesc_sw128(v_base + st * Cfg::kVStage, 16, 1024);
+            const int rw = n % RD;
+            const uint64_t rdesc = sdesc_sw128(raw_base + rw * Cfg::kRawBytes, 16, 1024);
+            if (Cfg::kKeyRaw) wait(sm.raw_full[rw], n / RD, PW_RAW);
 #pragma unroll
             for (int ks = 0; ks < (D + 64) / 16; ++ks) {
               const uint64_t qd = desc_add(qdesc, (ks >> 2) * Cfg::kQBox + (ks & 3) * 32);
-              if (Cfg::kTS || ks >= D / 16)
-                umma_ts(tbase + N * sb, ktm + 8 * (Cfg::kTS ? ks : ks - D / 16), qd, id, ks ? 1u : 0u);
-              else
-                umma_ss(tbase + N * sb, desc_add(kdesc, (ks >> 2) * kBox + (ks & 3) * 32), qd, id, ks ? 1u : 0u);
+              if (ks < D / 16) {
+                if (Cfg::kTS)
+                  umma_ts(tbase + N * sb, ktm + 8 * ks, qd, id, ks ? 1u : 0u);
+                else
+                  umma_ss(tbase + N * sb, desc_add(kdesc, (ks >> 2) * kBox + (ks & 3) * 32), qd, id, ks ? 1u : 0u);
+              } else if (Cfg::kKeyRaw) {
+                umma_ss(tbase + N * sb, desc_add(rdesc, (ks & 3) * 32), qd, id, 1u);
+              } else {
+                umma_ts(tbase + N * sb, ktm + 8 * (Cfg::kTS ? ks : ks - D / 16), qd, id, 1u);
+              }
             }
+            if (Cfg::kKeyRaw) umma_commit(smem_u32(&sm.raw_free[rw]));
             umma_commit(smem_u32(&sm.s_full[sb]));
           }
         }
@@ -514,89 +554,119 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
       const WaitCtl dc{&zero, p.err, p.wait_limit_ns};
       mbar_wait(smem_u32(&sm.drain), 0, dc, kPagedSite + PW_DRAIN);
     }
+  } else if (warp == 2) {
+    // ================================================================== copies
+    // A tile's rows in boxes of box_rows within one page, lane i the boxes i, i + 32, ..; a box that lies behind the
+    // request's end or has no page is not copied.  Boxes of fewer than eight rows would break the 128-byte alignment
+    // that a tensor copy wants of codes and scales in shared memory: those go row by row as plain bulk copies.
+    if constexpr (Cfg::kTma) {
+      PagedCursor& walk = sm.walk[kPagedSoft];
+      PagedSegment& seg = sm.conv_seg[0];
+      if (lane == 0) walk = sm.cur;
+      struct Tile {
+        int t, L, group;  // t < 0: none
+        const int* table;
+      };
+      int walk_t = 0, walk_hi = 0;
+      auto next_tile = [&]() -> Tile {
+        if (walk_t >= walk_hi) {
+          if (!paged_next(p, N, walk, seg, lane)) return Tile{-1, 0, 0, nullptr};
+          walk_t = seg.tile_lo;
+          walk_hi = seg.tile_hi;
+        }
+        return Tile{walk_t++, seg.L, seg.group, p.pages.table + seg.b * p.pages.table_stride};
+      };
+      // the page of the row `at` of a tile, -1 where there is none, and its slot there
+      auto find = [&](const Tile& x, int at, int& slot) -> int {
+        const int key = x.t * TN + at;
+        if (x.t < 0 || at >= TN || key >= x.L) return -1;
+        const int k = p.pages.page_shift >= 0 ? key >> p.pages.page_shift : key / p.pages.page_size;
+        slot = key - k * p.pages.page_size;
+        return k < p.pages.max_pages ? __ldg(x.table + k) : -1;
+      };
+      const int r = p.G * D, rows = p.box_rows;
+      const int key_at = int4_rope_at(r);
+      int n = 0, slot = 0;
+      Tile x = next_tile();
+      int page = find(x, lane * rows, slot);
+      for (; x.t >= 0; ++n) {
+        // the next tile's pages are asked for ahead of this one's wait
+        const Tile y = next_tile();
+        int slot_y = 0;
+        const int page_y = find(y, lane * rows, slot_y);
+        const int rw = n % RD;
+        const uint32_t bar = smem_u32(&sm.raw_full[rw]), dst = raw_base + rw * Cfg::kRawBytes;
+        const int code_at = x.group * (D / 2), scale_at = r / 2 + (x.group * (D / 16) & ~15);
+        const int odd = x.group & 1 ? PK_ODD_GROUP : 0;
+        if (n >= RD) wait(sm.raw_free[rw], n / RD - 1, PW_RAWFREE);
+        if (__any_sync(0xffffffffu, *const_cast<volatile uint32_t*>(&sm.abort) != 0)) break;
+        for (int i0 = 0; i0 * rows < TN; i0 += 32) {
+          const int at = (i0 + lane) * rows, first = x.t * TN + at;
+          if (i0 > 0) page = find(x, at, slot);
+          const bool token = at < TN && first < x.L;
+          if (token && (page < 0 || page >= p.pages.n_pages)) {
+            record_error(p.err, LKV_SITE_BAD_ROW);
+            page = -1;
+          }
+          // the keys' states, four to a word
+          const unsigned some = __ballot_sync(0xffffffffu, page >= 0);
+          if (rows > 1) {
+            const int state = (some >> (4 * lane / rows) & 1 ? PK_ROW : PK_NO_PAGE) | odd, left = x.L - x.t * TN - 4 * lane;
+            uint32_t w = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w |= static_cast<uint32_t>(j < left ? state : PK_END) << (8 * j);
+            *reinterpret_cast<uint32_t*>(&sm.state[rw][4 * lane]) = w;
+          } else {
+            sm.state[rw][at] = !token ? PK_END : (page < 0 ? PK_NO_PAGE : PK_ROW) | odd;
+          }
+          // the barrier learns of these copies' bytes before they can land, and of the tile's last ones with the
+          // arrival that it waits for
+          const uint32_t bytes = __popc(some) * rows * (128 + D / 2 + 16);
+          __syncwarp();
+          if (lane == 0) {
+            if ((i0 + 32) * rows < TN)
+              mbar_expect_tx(bar, bytes);
+            else
+              mbar_arrive_expect_tx(bar, bytes);
+          }
+          __syncwarp();
+          if (page >= 0) {
+            const uint32_t codes = dst + kBox + at * (D / 2), scales = dst + kBox + Cfg::kCodeBytes + at * 16;
+            tma_load_3d(dst + at * 128, &maps.keys, bar, key_at, slot, page);
+            if (rows > 1) {
+              tma_load_3d(codes, &maps.codes, bar, code_at, slot, page);
+              tma_load_3d(scales, &maps.scales, bar, scale_at, slot, page);
+            } else {
+              const uint8_t* row = p.pages.pool + page * p.pages.page_stride + slot * p.pages.row_stride;
+              bulk_load(codes, row + code_at, D / 2, bar);
+              bulk_load(scales, row + scale_at, 16, bar);
+            }
+          }
+        }
+        x = y;
+        page = page_y;
+        slot = slot_y;
+      }
+      // no copy may still be on its way when the block exits
+      uint32_t zero = 0;
+      const WaitCtl dc{&zero, p.err, p.wait_limit_ns};
+      for (int m = n > RD ? n - RD : 0; m < n; ++m) mbar_wait(smem_u32(&sm.raw_full[m % RD]), (m / RD) & 1, dc, kPagedSite + PW_RAW);
+    }
   } else if (warp >= 4 + kPagedSoft) {
     // ================================================================== converters
     // Warp w takes 16 keys of every tile: lanes 16 (w / 4) .. + 15 of the TMEM quadrant w % 4.  Thread 4g + 2h + b has
     // key g + 8b and of it the 32-column chunks h + 2m (m = 0, 1 in every 128 columns) and the 16-byte pieces h + 2m of
     // the RoPE key, which is how tcgen05.st 16x64b spreads a warp's registers; the K index of QK runs through the
-    // columns in that order, and Q is stored to match.  The next tile's loads are issued when this one is converted;
-    // its rows were asked into L2 a tile earlier, and their page numbers one tile earlier still.
+    // columns in that order, and Q is stored to match.  Where they load for themselves, the next tile's loads are issued
+    // when this one is converted; its rows were asked into L2 a tile earlier, and their page numbers one tile before.
     constexpr int kKeys = kPagedTile / kPagedConv, kH = D / 128;
     const int cw = warp - (4 + kPagedSoft), key0 = 32 * (cw & 3) + 16 * (cw >> 2);
     const int rr = (lane >> 2) + 8 * (lane & 1), hf = (lane >> 1) & 1;
     const int r = p.G * D;
     const uint8_t* pool = p.pages.pool;
     const int key_at = int4_rope_at(r);
-    struct Tile {
-      int b, t, L, group;  // t < 0: none
-    };
-    PagedCursor& walk = sm.walk[kPagedSoft + cw];
-    PagedSegment& seg = sm.conv_seg[cw];
-    if (lane == 0) walk = sm.cur;
-    int walk_t = 0, walk_hi = 0;
-    auto next_tile = [&]() -> Tile {
-      if (walk_t >= walk_hi) {
-        if (!paged_next(p, N, walk, seg, lane)) return Tile{0, -1, 0, 0};
-        walk_t = seg.tile_lo;
-        walk_hi = seg.tile_hi;
-      }
-      return Tile{seg.b, walk_t++, seg.L, seg.group};
-    };
-    // this lane's key of a tile (lanes 0 .. 15): the page is asked for here, used a tile later
-    int page = -1, slot = 0;
-    bool key_live = false;
-    auto ask_page = [&](const Tile& x) {
-      const int key = x.t * TN + key0 + lane;
-      key_live = x.t >= 0 && lane < kKeys && key < x.L;
-      page = -1;
-      if (key_live) {
-        const int k = p.pages.page_shift >= 0 ? key >> p.pages.page_shift : key / p.pages.page_size;
-        slot = key - k * p.pages.page_size;
-        if (k < p.pages.max_pages) page = __ldg(p.pages.table + x.b * p.pages.table_stride + k);
-      }
-    };
-    auto row_of_page = [&](const Tile& x) -> long long {
-      if (!key_live) return -1;
-      if (page < 0 || page >= p.pages.n_pages) {
-        record_error(p.err, LKV_SITE_BAD_ROW);
-        return -1;
-      }
-      const long long off = page * p.pages.page_stride + slot * p.pages.row_stride;
-      const uint8_t* row = pool + off;
-      prefetch_l2(row + x.group * (D / 2));
-      if (D == 512) prefetch_l2(row + x.group * (D / 2) + 128);
-      prefetch_l2(row + key_at);
-      return off;
-    };
     uint4 code[kH][2], key[4];
     uint32_t scale[2 * kH];  // of the chunks 2m and 2m + 1
-    auto load_rows = [&](long long off, int group) {
-      const long long at = __shfl_sync(0xffffffffu, off, rr);
-      const uint8_t* cp = pool + at + (16 * hf + group * (D / 2));
-      const uint8_t* sp = pool + at + (r / 2 + group * (D / 16));
-      const uint8_t* kp = pool + at + (16 * hf + key_at);
-      if (__all_sync(0xffffffffu, at >= 0) || at >= 0) {
-        static_for<kH>([&](auto h) {
-          code[h][0] = ldg16<64 * h>(cp);
-          code[h][1] = ldg16<64 * h + 32>(cp);
-        });
-        if constexpr (D == 128) {
-          const uint2 v = ldg8(sp);
-          scale[0] = v.x, scale[1] = v.y;
-        } else {
-          static_for<kH / 2>([&](auto h) {
-            const uint4 v = ldg16<16 * h>(sp);
-            scale[4 * h] = v.x, scale[4 * h + 1] = v.y, scale[4 * h + 2] = v.z, scale[4 * h + 3] = v.w;
-          });
-        }
-        static_for<4>([&](auto m) { key[m] = ldg16<32 * m>(kp); });
-      } else {  // no token: scales of 0 make any codes zeros, and the key is zeros
-#pragma unroll
-        for (int m = 0; m < 2 * kH; ++m) scale[m] = 0;
-#pragma unroll
-        for (int m = 0; m < 4; ++m) key[m] = make_uint4(0u, 0u, 0u, 0u);
-      }
-    };
     uint32_t mask = 0x000f000fu, magic = 0x43004300u;
     asm volatile("" : "+r"(mask), "+r"(magic));
     const uint32_t pick = hf ? 0x3232u : 0x1010u;  // this lane's scale of a pair, twice
@@ -607,18 +677,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
     const uint32_t tlane = tbase + K0 + (static_cast<uint32_t>(key0) << 16);
 #pragma unroll
     for (int h = 0; h < kH; ++h) code[h][0] = code[h][1] = make_uint4(0u, 0u, 0u, 0u);
-    Tile now = next_tile(), then = Tile{0, -1, 0, 0};
-    ask_page(now);
-    long long off_then = row_of_page(now);
-    if (now.t >= 0) {
-      load_rows(off_then, now.group);
-      then = next_tile();
-    }
-    ask_page(then);
-    off_then = row_of_page(then);
-    Tile later = then.t >= 0 ? next_tile() : then;
-    ask_page(later);
-    for (int n = 0; now.t >= 0; ++n) {
+    // one tile's registers to the value operand and, where QK wants it there, to TMEM
+    auto convert = [&](int n) {
       const int st = n % ST;
       if (n >= ST) wait(sm.empty[st], n / ST - 1, PW_EMPTY);
       tc_fence_after();
@@ -645,25 +705,151 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
           if (Cfg::kTS) tmem_st_16x64_x16(ktm + 64 * h + 32 * m, out);
         }
       }
-      {
+      if constexpr (!Cfg::kKeyRaw) {
         uint32_t out[16];
 #pragma unroll
         for (int m = 0; m < 4; ++m) out[4 * m] = key[m].x, out[4 * m + 1] = key[m].y, out[4 * m + 2] = key[m].z, out[4 * m + 3] = key[m].w;
         tmem_st_16x64_x16(ktm + (Cfg::kTS ? D / 2 : 0), out);
       }
       tmem_wait_st();
-      fence_proxy_async_smem();  // ahead of the loads: its memory barrier would wait for them
+      fence_proxy_async_smem();  // ahead of the next global loads: its memory barrier would wait for them
       tc_fence_before();
       warp_arrive(sm.full[st]);
-      if (then.t >= 0) load_rows(off_then, then.group);
-      now = then;
-      then = later;
+    };
+    if constexpr (Cfg::kTma) {
+      const int tiles = static_cast<int>(sm.cur.t_end - sm.cur.t_begin);
+      for (int n = 0; n < tiles; ++n) {
+        const int rw = n % RD;
+        uint8_t* tile = raw + rw * Cfg::kRawBytes;
+        uint8_t* key_row = tile + (key0 + rr) * 128;
+        const uint8_t* cp = tile + kBox + (key0 + rr) * (D / 2) + 16 * hf;
+        const uint8_t* sp = tile + kBox + Cfg::kCodeBytes + (key0 + rr) * 16;
+        wait(sm.raw_full[rw], n / RD, PW_RAW);
+        const int state = sm.state[rw][key0 + rr];
+        static_for<kH>([&](auto h) {
+          code[h][0] = *reinterpret_cast<const uint4*>(cp + 64 * h);
+          code[h][1] = *reinterpret_cast<const uint4*>(cp + 64 * h + 32);
+        });
+        if constexpr (D == 128) {
+          const uint2 v = *reinterpret_cast<const uint2*>(sp + (state & PK_ODD_GROUP ? 8 : 0));
+          scale[0] = v.x, scale[1] = v.y;
+        } else {
+          const uint4 v = *reinterpret_cast<const uint4*>(sp);
+          scale[0] = v.x, scale[1] = v.y, scale[2] = v.z, scale[3] = v.w;
+        }
+        if constexpr (!Cfg::kKeyRaw) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) key[m] = *reinterpret_cast<const uint4*>(key_row + (((hf + 2 * m) ^ (rr & 7)) << 4));
+        }
+        if (state & (PK_NO_PAGE | PK_END)) {  // scales of 0 make any codes zeros; behind the end the scores are not looked at
+#pragma unroll
+          for (int m = 0; m < 2 * kH; ++m) scale[m] = 0;
+          if (state & PK_NO_PAGE) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              if constexpr (Cfg::kKeyRaw)
+                *reinterpret_cast<uint4*>(key_row + 64 * hf + 16 * m) = make_uint4(0u, 0u, 0u, 0u);
+              else
+                key[m] = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+        }
+        warp_arrive(sm.raw_free[rw]);
+        convert(n);
+      }
+    } else {
+      struct Tile {
+        int b, t, L, group;  // t < 0: none
+      };
+      PagedCursor& walk = sm.walk[kPagedSoft + cw];
+      PagedSegment& seg = sm.conv_seg[cw];
+      if (lane == 0) walk = sm.cur;
+      int walk_t = 0, walk_hi = 0;
+      auto next_tile = [&]() -> Tile {
+        if (walk_t >= walk_hi) {
+          if (!paged_next(p, N, walk, seg, lane)) return Tile{0, -1, 0, 0};
+          walk_t = seg.tile_lo;
+          walk_hi = seg.tile_hi;
+        }
+        return Tile{seg.b, walk_t++, seg.L, seg.group};
+      };
+      // this lane's key of a tile (lanes 0 .. 15): the page is asked for here, used a tile later
+      int page = -1, slot = 0;
+      bool key_live = false;
+      auto ask_page = [&](const Tile& x) {
+        const int key = x.t * TN + key0 + lane;
+        key_live = x.t >= 0 && lane < kKeys && key < x.L;
+        page = -1;
+        if (key_live) {
+          const int k = p.pages.page_shift >= 0 ? key >> p.pages.page_shift : key / p.pages.page_size;
+          slot = key - k * p.pages.page_size;
+          if (k < p.pages.max_pages) page = __ldg(p.pages.table + x.b * p.pages.table_stride + k);
+        }
+      };
+      auto row_of_page = [&](const Tile& x) -> long long {
+        if (!key_live) return -1;
+        if (page < 0 || page >= p.pages.n_pages) {
+          record_error(p.err, LKV_SITE_BAD_ROW);
+          return -1;
+        }
+        const long long off = page * p.pages.page_stride + slot * p.pages.row_stride;
+        const uint8_t* row = pool + off;
+        prefetch_l2(row + x.group * (D / 2));
+        if (D == 512) prefetch_l2(row + x.group * (D / 2) + 128);
+        prefetch_l2(row + key_at);
+        return off;
+      };
+      auto load_rows = [&](long long off, int group) {
+        const long long at = __shfl_sync(0xffffffffu, off, rr);
+        const uint8_t* cp = pool + at + (16 * hf + group * (D / 2));
+        const uint8_t* sp = pool + at + (r / 2 + group * (D / 16));
+        const uint8_t* kp = pool + at + (16 * hf + key_at);
+        if (__all_sync(0xffffffffu, at >= 0) || at >= 0) {
+          static_for<kH>([&](auto h) {
+            code[h][0] = ldg16<64 * h>(cp);
+            code[h][1] = ldg16<64 * h + 32>(cp);
+          });
+          if constexpr (D == 128) {
+            const uint2 v = ldg8(sp);
+            scale[0] = v.x, scale[1] = v.y;
+          } else {
+            static_for<kH / 2>([&](auto h) {
+              const uint4 v = ldg16<16 * h>(sp);
+              scale[4 * h] = v.x, scale[4 * h + 1] = v.y, scale[4 * h + 2] = v.z, scale[4 * h + 3] = v.w;
+            });
+          }
+          static_for<4>([&](auto m) { key[m] = ldg16<32 * m>(kp); });
+        } else {  // no token: scales of 0 make any codes zeros, and the key is zeros
+#pragma unroll
+          for (int m = 0; m < 2 * kH; ++m) scale[m] = 0;
+#pragma unroll
+          for (int m = 0; m < 4; ++m) key[m] = make_uint4(0u, 0u, 0u, 0u);
+        }
+      };
+      Tile now = next_tile();
+      ask_page(now);
+      long long off_then = row_of_page(now);
+      Tile then = Tile{0, -1, 0, 0};
+      if (now.t >= 0) {
+        load_rows(off_then, now.group);
+        then = next_tile();
+      }
+      ask_page(then);
       off_then = row_of_page(then);
-      if (then.t >= 0) later = next_tile();
+      Tile later = then.t >= 0 ? next_tile() : then;
       ask_page(later);
+      for (int n = 0; now.t >= 0; ++n) {
+        convert(n);
+        if (then.t >= 0) load_rows(off_then, then.group);
+        now = then;
+        then = later;
+        off_then = row_of_page(then);
+        if (then.t >= 0) later = next_tile();
+        ask_page(later);
+      }
     }
   } else if (warp >= 4) {
-    // ================================================================== softmax / epilogue (warps 2 and 3 are idle)
+    // ================================================================== softmax / epilogue (warp 3 is idle)
     const int sw = warp - 4;
     const int q4 = warp & 3;                     // TMEM lane quadrant
     const int set = sw >> 2;
