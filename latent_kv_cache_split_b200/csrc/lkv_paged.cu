@@ -124,7 +124,7 @@ lkv_status launch_decode(const PagedDecodeParams& p, cudaStream_t s) {
     auto map = [&](CUtensorMap* m, uint32_t bytes, CUtensorMapSwizzle sw) {
       return make_tmap_u8_3d(m, g.pool, rb, g.page_size, g.n_pages, g.row_stride, ps, bytes, p.box_rows, sw);
     };
-    if (!map(&maps.codes, D / 2, CU_TENSOR_MAP_SWIZZLE_NONE) || !map(&maps.scales, 16, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+    if (!map(&maps.codes, D / 2, PagedCfg<D, N>::kWide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE) || !map(&maps.scales, 16, CU_TENSOR_MAP_SWIZZLE_NONE) ||
         !map(&maps.keys, 128, CU_TENSOR_MAP_SWIZZLE_128B))
       return LKV_ERR_UNSUPPORTED;  // strides past what a tensor map holds
   }

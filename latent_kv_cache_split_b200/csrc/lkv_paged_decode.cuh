@@ -173,6 +173,7 @@ struct PagedCfg {
   // QK reads the RoPE key from the raw tile (the copy leaves it as an MMA wants it) where the ring is deep enough to hold
   // the tile that long, else the converters put it into TMEM.
   static constexpr bool kKeyRaw = D == 128;
+  static constexpr bool kWide = D == 256;  // codes in rows of 128 bytes, which the copy swizzles
   static constexpr int kKCols = (kTS ? D / 2 : 0) + (kKeyRaw ? 0 : 32);  // TMEM columns of a stage: the key operand
   static constexpr int kStages = D == 128 ? 3 : D == 256 ? 2 : 1;
   static constexpr int kRaws = !kTma ? 1 : D == 256 ? (N == 16 ? 2 : 1) : N == 64 ? 2 : 3;  // raw tiles
@@ -252,6 +253,13 @@ __device__ __noinline__ void paged_wait_slow(uint32_t bar, uint32_t parity, vola
 template <bool kTS>
 __device__ __forceinline__ int paged_key_row(int k) {
   return kTS ? (k & ~14) | ((k >> 2) & 2) | ((k & 6) << 1) : k;
+}
+
+// The raw tile's row of the key in TMEM lane k: where the converters read 128-byte rows of codes and of RoPE keys, bits 0, 1, 2,
+// 3 of k move to 1, 0, 3, 2, so that eight neighbouring lanes read eight different 16-byte columns of the swizzled rows.
+template <bool kWide>
+__device__ __forceinline__ int paged_raw_row(int k) {
+  return kWide ? (k & ~15) | ((k >> 1) & 5) | ((k << 1) & 10) : k;
 }
 
 template <int RW>
@@ -633,14 +641,15 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
           if (page >= 0) {
             const uint32_t codes = dst + kBox + at * (D / 2), scales = dst + kBox + Cfg::kCodeBytes + at * 16;
             tma_load_3d(dst + at * 128, &maps.keys, bar, key_at, slot, page);
-            if (rows > 1) {
+            const uint8_t* row = p.pages.pool + page * p.pages.page_stride + slot * p.pages.row_stride;
+            if (rows > 1 || Cfg::kWide)
               tma_load_3d(codes, &maps.codes, bar, code_at, slot, page);
-              tma_load_3d(scales, &maps.scales, bar, scale_at, slot, page);
-            } else {
-              const uint8_t* row = p.pages.pool + page * p.pages.page_stride + slot * p.pages.row_stride;
+            else
               bulk_load(codes, row + code_at, D / 2, bar);
+            if (rows > 1)
+              tma_load_3d(scales, &maps.scales, bar, scale_at, slot, page);
+            else
               bulk_load(scales, row + scale_at, 16, bar);
-            }
           }
         }
         x = y;
@@ -718,17 +727,18 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
     };
     if constexpr (Cfg::kTma) {
       const int tiles = static_cast<int>(sm.cur.t_end - sm.cur.t_begin);
+      const int raw_row = key0 + paged_raw_row<Cfg::kWide>(rr), x8 = Cfg::kWide ? raw_row & 7 : 0;
       for (int n = 0; n < tiles; ++n) {
         const int rw = n % RD;
         uint8_t* tile = raw + rw * Cfg::kRawBytes;
-        uint8_t* key_row = tile + (key0 + rr) * 128;
-        const uint8_t* cp = tile + kBox + (key0 + rr) * (D / 2) + 16 * hf;
-        const uint8_t* sp = tile + kBox + Cfg::kCodeBytes + (key0 + rr) * 16;
+        uint8_t* key_row = tile + raw_row * 128;
+        const uint8_t* cp = tile + kBox + raw_row * (D / 2);
+        const uint8_t* sp = tile + kBox + Cfg::kCodeBytes + raw_row * 16;
         wait(sm.raw_full[rw], n / RD, PW_RAW);
-        const int state = sm.state[rw][key0 + rr];
+        const int state = sm.state[rw][raw_row];
         static_for<kH>([&](auto h) {
-          code[h][0] = *reinterpret_cast<const uint4*>(cp + 64 * h);
-          code[h][1] = *reinterpret_cast<const uint4*>(cp + 64 * h + 32);
+          code[h][0] = *reinterpret_cast<const uint4*>(cp + (((4 * h + hf) ^ x8) << 4));
+          code[h][1] = *reinterpret_cast<const uint4*>(cp + (((4 * h + 2 + hf) ^ x8) << 4));
         });
         if constexpr (D == 128) {
           const uint2 v = *reinterpret_cast<const uint2*>(sp + (state & PK_ODD_GROUP ? 8 : 0));
@@ -739,7 +749,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
         }
         if constexpr (!Cfg::kKeyRaw) {
 #pragma unroll
-          for (int m = 0; m < 4; ++m) key[m] = *reinterpret_cast<const uint4*>(key_row + (((hf + 2 * m) ^ (rr & 7)) << 4));
+          for (int m = 0; m < 4; ++m) key[m] = *reinterpret_cast<const uint4*>(key_row + (((hf + 2 * m) ^ x8) << 4));
         }
         if (state & (PK_NO_PAGE | PK_END)) {  // scales of 0 make any codes zeros; behind the end the scores are not looked at
 #pragma unroll
@@ -897,8 +907,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
       const PagedSegment& sg = sm.seg[sw][seg & 1];
       PagedSegment& nx = sm.seg[sw][(seg + 1) & 1];
       const int tiles = sg.tile_hi - sg.tile_lo;
-      const int lim0 = sg.L - p.s_q - sg.tile_lo * TN - k;  // query i sees this thread's key of tile j where 128 j <= lim0 + i
-      const int whole = lim0 + k - (TN - 1);                // 128 j <= whole: every query sees all keys of the tile
+      const int key = paged_raw_row<Cfg::kWide>(k);
+      const int lim0 = sg.L - p.s_q - sg.tile_lo * TN - key;  // query i sees this thread's key of tile j where 128 j <= lim0 + i
+      const int whole = lim0 + key - (TN - 1);                // 128 j <= whole: every query sees all keys of the tile
       const int newest = p.hpg - (sg.row0 + rb);            // rows from here on are query 1's (or padding)
       float m_run = 0.f;                                    // reference of row rb + rl (log2 units)
 #pragma unroll
