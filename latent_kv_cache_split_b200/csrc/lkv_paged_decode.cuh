@@ -176,6 +176,9 @@ struct PagedCfg {
   static constexpr bool kWide = D == 256;  // codes in rows of 128 bytes, which the copy swizzles
   static constexpr int kKCols = (kTS ? D / 2 : 0) + (kKeyRaw ? 0 : 32);  // TMEM columns of a stage: the key operand
   static constexpr int kStages = D == 128 ? 3 : D == 256 ? 2 : 1;
+  // A stage is handed on in blocks: the one stage of D = 512 by 128 columns, so that QK starts on the first columns while the
+  // rest is converted, and the next tile's conversion while PV runs over the last columns.
+  static constexpr int kBlocks = D == 512 ? 4 : 1;
   static constexpr int kRaws = !kTma ? 1 : D == 256 ? (N == 16 ? 2 : 1) : N == 64 ? 2 : 3;  // raw tiles
   static constexpr int kCodeBytes = kPagedTile * (D / 2), kScaleBytes = kPagedTile * 16;
   static constexpr int kRawBytes = kTma ? kBox + kCodeBytes + kScaleBytes : 0;  // RoPE keys, codes, scales
@@ -201,9 +204,9 @@ struct PagedCfg {
 constexpr int kPagedSite = LKV_SITE_WAIT_BASE + 300;  // wait sites of this kernel
 enum PagedWaitSite { PW_EMPTY = 1, PW_RAW, PW_RAWFREE, PW_FULL, PW_SFREE, PW_QREADY, PW_PFULL, PW_OFREE, PW_SFULL, PW_ODONE, PW_VOTE, PW_XCHG, PW_FIN, PW_DRAIN };
 
-template <int RW, int N, int NG, int NC, int ST, int RD>
+template <int RW, int N, int NG, int NC, int FULL, int RD>
 struct __align__(16) PagedSmem {
-  uint64_t full[ST], empty[ST];
+  uint64_t full[FULL], empty[FULL];  // of a stage's block
   uint64_t raw_full[RD], raw_free[RD];
   uint64_t s_full[2], s_free[2], p_full[2], o_done[2];
   uint64_t vote_bar[2], xchg_bar[2];  // of a softmax group
@@ -420,14 +423,14 @@ template <int D, int N>
 __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __grid_constant__ PagedDecodeParams p,
                                                                            const __grid_constant__ PagedMaps maps) {
   using Cfg = PagedCfg<D, N>;
-  constexpr int TN = kPagedTile, ST = Cfg::kStages, SS = Cfg::kSBufs, PS = Cfg::kPs;
+  constexpr int TN = kPagedTile, ST = Cfg::kStages, BL = Cfg::kBlocks, SS = Cfg::kSBufs, PS = Cfg::kPs;
   constexpr int RW = Cfg::kRW, MB = Cfg::kMB, NG = Cfg::kGroups, GW = Cfg::kGW;
   constexpr int kBox = Cfg::kBox;
   constexpr uint32_t O0 = Cfg::kO0, K0 = Cfg::kK0;
 
   extern __shared__ __align__(1024) uint8_t paged_smem_raw[];
   constexpr int RD = Cfg::kRaws;
-  __shared__ PagedSmem<RW, N, NG, Cfg::kTma ? 1 : kPagedConv, ST, RD> sm;
+  __shared__ PagedSmem<RW, N, NG, Cfg::kTma ? 1 : kPagedConv, ST * BL, RD> sm;
   static_assert(Cfg::kSmem + sizeof(sm) <= 232448, "shared memory budget");
   uint8_t* dsm = paged_smem_raw + ((1024u - (smem_u32(paged_smem_raw) & 1023u)) & 1023u);
   uint8_t* raw = dsm + ST * Cfg::kVStage;
@@ -438,7 +441,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
   const int range = blockIdx.x;
 
   if (tid == 0) {
-    for (int s = 0; s < ST; ++s) {
+    for (int s = 0; s < ST * BL; ++s) {
       mbar_init(smem_u32(&sm.full[s]), kPagedConv);
       mbar_init(smem_u32(&sm.empty[s]), 1);
     }
@@ -500,7 +503,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
         for (; cur.next(p, N, sg) && !aborted(); ++seg) {
           for (int t = sg.tile_lo; t < sg.tile_hi; ++t, ++n) {
             const int sb = n % SS, st = n % ST;
-            wait(sm.full[st], n / ST, PW_FULL);
+            wait(sm.full[st * BL], n / ST, PW_FULL);
             if (n >= SS) wait(sm.s_free[sb], n / SS - 1, PW_SFREE);
             if (t == sg.tile_lo) wait(sm.q_ready, seg, PW_QREADY);
             if (aborted()) break;
@@ -512,6 +515,11 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
             if (Cfg::kKeyRaw) wait(sm.raw_full[rw], n / RD, PW_RAW);
 #pragma unroll
             for (int ks = 0; ks < (D + 64) / 16; ++ks) {
+              constexpr int kStep = D / 16 / BL;  // MMAs of a block
+              if (BL > 1 && ks > 0 && ks < D / 16 && ks % kStep == 0) {
+                wait(sm.full[st * BL + ks / kStep], n / ST, PW_FULL);
+                tc_fence_after();
+              }
               const uint64_t qd = desc_add(qdesc, (ks >> 2) * Cfg::kQBox + (ks & 3) * 32);
               if (ks < D / 16) {
                 if (Cfg::kTS)
@@ -550,9 +558,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
 #pragma unroll
               for (int kk = 0; kk < TN / 16; ++kk)
                 umma_ss(od + N * mb, desc_add(vdesc, kk * 2048), desc_add(pdesc, kk * 2 * atom), id, first && kk == 0 ? 0u : 1u);
+              if (BL == MB && mb + 1 < MB) umma_commit(smem_u32(&sm.empty[st * BL + mb]));
             }
             umma_commit(smem_u32(&sm.o_done[pb]));
-            umma_commit(smem_u32(&sm.empty[st]));
+            umma_commit(smem_u32(&sm.empty[st * BL + BL - 1]));
           }
         }
       }
@@ -655,6 +664,12 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
         x = y;
         page = page_y;
         slot = slot_y;
+        // with a single raw tile its copies wait for the converters: the rows can come as far as L2 meanwhile (GLA-2: 265 -> 259 us)
+        if (RD == 1 && rows > 1 && page >= 0 && page < p.pages.n_pages) {
+          tma_prefetch_3d(&maps.keys, key_at, slot, page);
+          tma_prefetch_3d(&maps.codes, x.group * (D / 2), slot, page);
+          tma_prefetch_3d(&maps.scales, r / 2 + (x.group * (D / 16) & ~15), slot, page);
+        }
       }
       // no copy may still be on its way when the block exits
       uint32_t zero = 0;
@@ -689,12 +704,22 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
     // one tile's registers to the value operand and, where QK wants it there, to TMEM
     auto convert = [&](int n) {
       const int st = n % ST;
-      if (n >= ST) wait(sm.empty[st], n / ST - 1, PW_EMPTY);
+      if (n >= ST) wait(sm.empty[st * BL], n / ST - 1, PW_EMPTY);
       tc_fence_after();
       uint8_t* stage = dsm + st * Cfg::kVStage;
       const uint32_t ktm = tlane + st * Cfg::kKCols;
+      if constexpr (!Cfg::kKeyRaw) {
+        uint32_t out[16];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) out[4 * m] = key[m].x, out[4 * m + 1] = key[m].y, out[4 * m + 2] = key[m].z, out[4 * m + 3] = key[m].w;
+        tmem_st_16x64_x16(ktm + (Cfg::kTS ? D / 2 : 0), out);
+      }
 #pragma unroll
       for (int h = 0; h < kH; ++h) {
+        if (BL > 1 && h > 0 && n >= ST) {
+          wait(sm.empty[st * BL + h], n / ST - 1, PW_EMPTY);
+          tc_fence_after();
+        }
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           uint32_t out[16];
@@ -713,17 +738,13 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
           }
           if (Cfg::kTS) tmem_st_16x64_x16(ktm + 64 * h + 32 * m, out);
         }
+        if (BL > 1 || h == kH - 1) {
+          if (BL == 1 || h == 0) tmem_wait_st();
+          fence_proxy_async_smem();  // ahead of the next global loads: its memory barrier would wait for them
+          tc_fence_before();
+          warp_arrive(sm.full[st * BL + (BL > 1 ? h : 0)]);
+        }
       }
-      if constexpr (!Cfg::kKeyRaw) {
-        uint32_t out[16];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) out[4 * m] = key[m].x, out[4 * m + 1] = key[m].y, out[4 * m + 2] = key[m].z, out[4 * m + 3] = key[m].w;
-        tmem_st_16x64_x16(ktm + (Cfg::kTS ? D / 2 : 0), out);
-      }
-      tmem_wait_st();
-      fence_proxy_async_smem();  // ahead of the next global loads: its memory barrier would wait for them
-      tc_fence_before();
-      warp_arrive(sm.full[st]);
     };
     if constexpr (Cfg::kTma) {
       const int tiles = static_cast<int>(sm.cur.t_end - sm.cur.t_begin);
