@@ -174,6 +174,10 @@ struct PagedCfg {
   // the tile that long, else the converters put it into TMEM.
   static constexpr bool kKeyRaw = D == 128;
   static constexpr bool kWide = D == 256;  // codes in rows of 128 bytes, which the copy swizzles
+  // Converters: two groups that take turns at the tiles with 32 keys a warp, or one with 16 keys a warp of every tile.  A warp's
+  // tile is a chain of waits, reads, stores and fences whose length hardly depends on the keys.
+  static constexpr int kTurns = D == 128 ? 2 : 1;
+  static constexpr int kCW = kPagedConv / kTurns;  // warps of a group
   static constexpr int kKCols = (kTS ? D / 2 : 0) + (kKeyRaw ? 0 : 32);  // TMEM columns of a stage: the key operand
   static constexpr int kStages = D == 128 ? 3 : D == 256 ? 2 : 1;
   // A stage is handed on in blocks: the one stage of D = 512 by 128 columns, so that QK starts on the first columns while the
@@ -207,7 +211,7 @@ enum PagedWaitSite { PW_EMPTY = 1, PW_RAW, PW_RAWFREE, PW_FULL, PW_SFREE, PW_QRE
 template <int RW, int N, int NG, int NC, int FULL, int RD>
 struct __align__(16) PagedSmem {
   uint64_t full[FULL], empty[FULL];  // of a stage's block
-  uint64_t raw_full[RD], raw_free[RD];
+  uint64_t raw_full[2 * RD], raw_free[RD];  // two a raw tile, for its uses in turn: a group may wait a use ahead of the other's
   uint64_t s_full[2], s_free[2], p_full[2], o_done[2];
   uint64_t vote_bar[2], xchg_bar[2];  // of a softmax group
   uint64_t q_ready, o_free, fin_bar, drain;
@@ -442,12 +446,13 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
 
   if (tid == 0) {
     for (int s = 0; s < ST * BL; ++s) {
-      mbar_init(smem_u32(&sm.full[s]), kPagedConv);
+      mbar_init(smem_u32(&sm.full[s]), Cfg::kCW);
       mbar_init(smem_u32(&sm.empty[s]), 1);
     }
     for (int s = 0; s < RD; ++s) {
-      mbar_init(smem_u32(&sm.raw_full[s]), 1);
-      mbar_init(smem_u32(&sm.raw_free[s]), kPagedConv + Cfg::kKeyRaw);  // the converters' reads, and QK
+      mbar_init(smem_u32(&sm.raw_full[2 * s]), 1);
+      mbar_init(smem_u32(&sm.raw_full[2 * s + 1]), 1);
+      mbar_init(smem_u32(&sm.raw_free[s]), Cfg::kCW + Cfg::kKeyRaw);  // the converters' reads, and QK
     }
     for (int s = 0; s < 3; ++s) sm.vote[0][s] = sm.vote[1][s] = 0;
     for (int b = 0; b < 2; ++b) {
@@ -484,6 +489,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
     const uint32_t a = smem_u32(&bar), par = static_cast<uint32_t>(phase & 1);
     if (!mbar_test(a, par)) paged_wait_slow(a, par, &sm.abort, p.err, p.wait_limit_ns, kPagedSite + site);
   };
+  auto raw_full = [&](int n) -> uint64_t& { return sm.raw_full[2 * (n % RD) + (n / RD & 1)]; };  // tile n's, in its phase n / 2RD
   auto warp_arrive = [&](uint64_t& bar) {
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&bar));
@@ -512,7 +518,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
             const uint64_t kdesc = sdesc_sw128(v_base + st * Cfg::kVStage, 16, 1024);
             const int rw = n % RD;
             const uint64_t rdesc = sdesc_sw128(raw_base + rw * Cfg::kRawBytes, 16, 1024);
-            if (Cfg::kKeyRaw) wait(sm.raw_full[rw], n / RD, PW_RAW);
+            if (Cfg::kKeyRaw) wait(raw_full(n), n / (2 * RD), PW_RAW);
 #pragma unroll
             for (int ks = 0; ks < (D + 64) / 16; ++ks) {
               constexpr int kStep = D / 16 / BL;  // MMAs of a block
@@ -612,7 +618,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
         int slot_y = 0;
         const int page_y = find(y, lane * rows, slot_y);
         const int rw = n % RD;
-        const uint32_t bar = smem_u32(&sm.raw_full[rw]), dst = raw_base + rw * Cfg::kRawBytes;
+        const uint32_t bar = smem_u32(&raw_full(n)), dst = raw_base + rw * Cfg::kRawBytes;
         const int code_at = x.group * (D / 2), scale_at = r / 2 + (x.group * (D / 16) & ~15);
         const int odd = x.group & 1 ? PK_ODD_GROUP : 0;
         if (n >= RD) wait(sm.raw_free[rw], n / RD - 1, PW_RAWFREE);
@@ -674,7 +680,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
       // no copy may still be on its way when the block exits
       uint32_t zero = 0;
       const WaitCtl dc{&zero, p.err, p.wait_limit_ns};
-      for (int m = n > RD ? n - RD : 0; m < n; ++m) mbar_wait(smem_u32(&sm.raw_full[m % RD]), (m / RD) & 1, dc, kPagedSite + PW_RAW);
+      for (int m = n > RD ? n - RD : 0; m < n; ++m) mbar_wait(smem_u32(&raw_full(m)), (m / (2 * RD)) & 1, dc, kPagedSite + PW_RAW);
     }
   } else if (warp >= 4 + kPagedSoft) {
     // ================================================================== converters
@@ -683,14 +689,14 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
     // the RoPE key, which is how tcgen05.st 16x64b spreads a warp's registers; the K index of QK runs through the
     // columns in that order, and Q is stored to match.  Where they load for themselves, the next tile's loads are issued
     // when this one is converted; its rows were asked into L2 a tile earlier, and their page numbers one tile before.
-    constexpr int kKeys = kPagedTile / kPagedConv, kH = D / 128;
-    const int cw = warp - (4 + kPagedSoft), key0 = 32 * (cw & 3) + 16 * (cw >> 2);
+    constexpr int kKeys = 16, kH = D / 128, kHalves = Cfg::kTurns;
+    const int cw = warp - (4 + kPagedSoft), turn = kHalves == 2 ? cw >> 2 : 0, key0 = 32 * (cw & 3) + 16 * (kHalves == 2 ? 0 : cw >> 2);
     const int rr = (lane >> 2) + 8 * (lane & 1), hf = (lane >> 1) & 1;
     const int r = p.G * D;
     const uint8_t* pool = p.pages.pool;
     const int key_at = int4_rope_at(r);
-    uint4 code[kH][2], key[4];
-    uint32_t scale[2 * kH];  // of the chunks 2m and 2m + 1
+    uint4 code[kHalves][kH][2], key[4];
+    uint32_t scale[kHalves][2 * kH];  // of the chunks 2m and 2m + 1
     uint32_t mask = 0x000f000fu, magic = 0x43004300u;
     asm volatile("" : "+r"(mask), "+r"(magic));
     const uint32_t pick = hf ? 0x3232u : 0x1010u;  // this lane's scale of a pair, twice
@@ -700,7 +706,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
     for (int e = 0; e < 4; ++e) at_word[e] = vrow * 128 + (((4 * hf + e) ^ (vrow & 7)) << 4);
     const uint32_t tlane = tbase + K0 + (static_cast<uint32_t>(key0) << 16);
 #pragma unroll
-    for (int h = 0; h < kH; ++h) code[h][0] = code[h][1] = make_uint4(0u, 0u, 0u, 0u);
+    for (int h = 0; h < kH; ++h) code[0][h][0] = code[0][h][1] = make_uint4(0u, 0u, 0u, 0u);
     // one tile's registers to the value operand and, where QK wants it there, to TMEM
     auto convert = [&](int n) {
       const int st = n % ST;
@@ -715,7 +721,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
         tmem_st_16x64_x16(ktm + (Cfg::kTS ? D / 2 : 0), out);
       }
 #pragma unroll
-      for (int h = 0; h < kH; ++h) {
+      for (int u = 0; u < kHalves * kH; ++u) {
+        const int h = u % kH, half = u / kH;  // 128 columns of 16 keys
         if (BL > 1 && h > 0 && n >= ST) {
           wait(sm.empty[st * BL + h], n / ST - 1, PW_EMPTY);
           tc_fence_after();
@@ -723,22 +730,22 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           uint32_t out[16];
-          const uint32_t s2 = __byte_perm(scale[2 * h + m], 0, pick);
+          const uint32_t s2 = __byte_perm(scale[half][2 * h + m], 0, pick);
           const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&s2);
           const __nv_bfloat162 o = __hmul2(s, __float2bfloat162_rn(-136.f));
-          const uint32_t word[4] = {code[h][m].x, code[h][m].y, code[h][m].z, code[h][m].w};
+          const uint32_t word[4] = {code[half][h][m].x, code[half][h][m].y, code[half][h][m].z, code[half][h][m].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint4 x = int4_expand(word[e], mask, magic, s, o);
-            *reinterpret_cast<uint4*>(stage + at_word[e] + (2 * h + m) * kBox) = x;
+            *reinterpret_cast<uint4*>(stage + at_word[e] + half * 2048 + (2 * h + m) * kBox) = x;
             out[4 * e] = x.x;
             out[4 * e + 1] = x.y;
             out[4 * e + 2] = x.z;
             out[4 * e + 3] = x.w;
           }
-          if (Cfg::kTS) tmem_st_16x64_x16(ktm + 64 * h + 32 * m, out);
+          if (Cfg::kTS) tmem_st_16x64_x16(ktm + (half << 20) + 64 * h + 32 * m, out);
         }
-        if (BL > 1 || h == kH - 1) {
+        if (BL > 1 || u == kHalves * kH - 1) {
           if (BL == 1 || h == 0) tmem_wait_st();
           fence_proxy_async_smem();  // ahead of the next global loads: its memory barrier would wait for them
           tc_fence_before();
@@ -749,39 +756,44 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
     if constexpr (Cfg::kTma) {
       const int tiles = static_cast<int>(sm.cur.t_end - sm.cur.t_begin);
       const int raw_row = key0 + paged_raw_row<Cfg::kWide>(rr), x8 = Cfg::kWide ? raw_row & 7 : 0;
-      for (int n = 0; n < tiles; ++n) {
+      for (int n = turn; n < tiles; n += Cfg::kTurns) {
         const int rw = n % RD;
         uint8_t* tile = raw + rw * Cfg::kRawBytes;
-        uint8_t* key_row = tile + raw_row * 128;
-        const uint8_t* cp = tile + kBox + raw_row * (D / 2);
-        const uint8_t* sp = tile + kBox + Cfg::kCodeBytes + raw_row * 16;
-        wait(sm.raw_full[rw], n / RD, PW_RAW);
-        const int state = sm.state[rw][raw_row];
-        static_for<kH>([&](auto h) {
-          code[h][0] = *reinterpret_cast<const uint4*>(cp + (((4 * h + hf) ^ x8) << 4));
-          code[h][1] = *reinterpret_cast<const uint4*>(cp + (((4 * h + 2 + hf) ^ x8) << 4));
-        });
-        if constexpr (D == 128) {
-          const uint2 v = *reinterpret_cast<const uint2*>(sp + (state & PK_ODD_GROUP ? 8 : 0));
-          scale[0] = v.x, scale[1] = v.y;
-        } else {
-          const uint4 v = *reinterpret_cast<const uint4*>(sp);
-          scale[0] = v.x, scale[1] = v.y, scale[2] = v.z, scale[3] = v.w;
-        }
-        if constexpr (!Cfg::kKeyRaw) {
+        wait(raw_full(n), n / (2 * RD), PW_RAW);
 #pragma unroll
-          for (int m = 0; m < 4; ++m) key[m] = *reinterpret_cast<const uint4*>(key_row + (((hf + 2 * m) ^ x8) << 4));
-        }
-        if (state & (PK_NO_PAGE | PK_END)) {  // scales of 0 make any codes zeros; behind the end the scores are not looked at
+        for (int half = 0; half < kHalves; ++half) {
+          const int row = raw_row + 16 * half;
+          uint8_t* key_row = tile + row * 128;
+          const uint8_t* cp = tile + kBox + row * (D / 2);
+          const uint8_t* sp = tile + kBox + Cfg::kCodeBytes + row * 16;
+          const int state = sm.state[rw][row];
 #pragma unroll
-          for (int m = 0; m < 2 * kH; ++m) scale[m] = 0;
-          if (state & PK_NO_PAGE) {
+          for (int h = 0; h < kH; ++h) {
+            code[half][h][0] = *reinterpret_cast<const uint4*>(cp + (((4 * h + hf) ^ x8) << 4));
+            code[half][h][1] = *reinterpret_cast<const uint4*>(cp + (((4 * h + 2 + hf) ^ x8) << 4));
+          }
+          if constexpr (D == 128) {
+            const uint2 v = *reinterpret_cast<const uint2*>(sp + (state & PK_ODD_GROUP ? 8 : 0));
+            scale[half][0] = v.x, scale[half][1] = v.y;
+          } else {
+            const uint4 v = *reinterpret_cast<const uint4*>(sp);
+            scale[half][0] = v.x, scale[half][1] = v.y, scale[half][2] = v.z, scale[half][3] = v.w;
+          }
+          if constexpr (!Cfg::kKeyRaw) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              if constexpr (Cfg::kKeyRaw)
-                *reinterpret_cast<uint4*>(key_row + 64 * hf + 16 * m) = make_uint4(0u, 0u, 0u, 0u);
-              else
-                key[m] = make_uint4(0u, 0u, 0u, 0u);
+            for (int m = 0; m < 4; ++m) key[m] = *reinterpret_cast<const uint4*>(key_row + (((hf + 2 * m) ^ x8) << 4));
+          }
+          if (state & (PK_NO_PAGE | PK_END)) {  // scales of 0 make any codes zeros; behind the end the scores are not looked at
+#pragma unroll
+            for (int m = 0; m < 2 * kH; ++m) scale[half][m] = 0;
+            if (state & PK_NO_PAGE) {
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                if constexpr (Cfg::kKeyRaw)
+                  *reinterpret_cast<uint4*>(key_row + 64 * hf + 16 * m) = make_uint4(0u, 0u, 0u, 0u);
+                else
+                  key[m] = make_uint4(0u, 0u, 0u, 0u);
+              }
             }
           }
         }
@@ -837,22 +849,22 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
         const uint8_t* kp = pool + at + (16 * hf + key_at);
         if (__all_sync(0xffffffffu, at >= 0) || at >= 0) {
           static_for<kH>([&](auto h) {
-            code[h][0] = ldg16<64 * h>(cp);
-            code[h][1] = ldg16<64 * h + 32>(cp);
+            code[0][h][0] = ldg16<64 * h>(cp);
+            code[0][h][1] = ldg16<64 * h + 32>(cp);
           });
           if constexpr (D == 128) {
             const uint2 v = ldg8(sp);
-            scale[0] = v.x, scale[1] = v.y;
+            scale[0][0] = v.x, scale[0][1] = v.y;
           } else {
             static_for<kH / 2>([&](auto h) {
               const uint4 v = ldg16<16 * h>(sp);
-              scale[4 * h] = v.x, scale[4 * h + 1] = v.y, scale[4 * h + 2] = v.z, scale[4 * h + 3] = v.w;
+              scale[0][4 * h] = v.x, scale[0][4 * h + 1] = v.y, scale[0][4 * h + 2] = v.z, scale[0][4 * h + 3] = v.w;
             });
           }
           static_for<4>([&](auto m) { key[m] = ldg16<32 * m>(kp); });
         } else {  // no token: scales of 0 make any codes zeros, and the key is zeros
 #pragma unroll
-          for (int m = 0; m < 2 * kH; ++m) scale[m] = 0;
+          for (int m = 0; m < 2 * kH; ++m) scale[0][m] = 0;
 #pragma unroll
           for (int m = 0; m < 4; ++m) key[m] = make_uint4(0u, 0u, 0u, 0u);
         }
