@@ -312,7 +312,7 @@ lkv_status lkv_latent_cache_append_fp8(const void* new_rows, int64_t new_row_str
  *   positions  [n_tok] int32;  freqs [rot / 2] fp64, radians a position (long-context scalings change
  *              freqs and gain).  Angles are taken in fp64, products in fp32.
  *   out        as x; the same array and strides (in place) or one that does not overlap x
- * rot even, at most 1024 (LKV_ERR_UNSUPPORTED); gain finite and > 0.  n_tok = 0 launches nothing.
+ * rot even, at most 1024, heads at most 2^20 (LKV_ERR_UNSUPPORTED); gain finite and > 0.  n_tok = 0 launches nothing.
  */
 lkv_status lkv_rope_rotate(const void* x, int64_t x_token_stride, int64_t x_head_stride,
                            const int32_t* positions, const double* freqs, int64_t n_tok, int heads, int d,
@@ -349,7 +349,8 @@ size_t lkv_int4_cache_row_bytes(int r, int d_rope);
  *             (rows from cu_new[batch] on are ignored); NULL: n_new / batch rows for every request
  *   freqs     [d_rope / 2] fp64 with `interleaved` and `gain` as above: the key is rotated to its
  *             position, which is the token's index; NULL: stored as it comes
- *   rows_out  NULL, or [n_new, r + d_rope] bf16: the values the cache now holds (may be new_rows itself)
+ *   rows_out  NULL, or [n_new, r + d_rope] bf16: the values the cache now holds (may be new_rows itself, with
+ *             its stride)
  * A row whose index would be negative (more new rows than seq_lens counts) is skipped; one without a
  * page (past the table, or a page outside [0, n_pages)) is skipped and recorded as LKV_SITE_BAD_ROW.
  * Two rows with the same place in one call race.
@@ -371,7 +372,9 @@ lkv_status lkv_paged_append_int4(const void* new_rows, int64_t new_row_stride, i
  * of a one-token request) gets out = 0 and lse = -inf.  A token without a page counts as a row of zeros
  * and is recorded as LKV_SITE_BAD_ROW.  Rows behind a request's last token are not read as values.
  * Implemented: d 128, 256 or 512, groups * d <= 1024, d_rope = 64, s_q 1 or 2, s_q * h_q / groups <= 256.
+ * Strides of the pool below 2^40 bytes (LKV_ERR_UNSUPPORTED).
  * workspace_bytes >= lkv_paged_decode_workspace_size(...) (host-only, no CUDA call; 0 on bad input).
+ * Calls that may run at the same time (other streams, captured graphs) need workspaces of their own.
  */
 size_t lkv_paged_decode_workspace_size(int batch, int s_q, int h_q, int groups, int d, int num_sms);
 lkv_status lkv_paged_decode_int4(const void* q, const void* q_rope, const void* pool,

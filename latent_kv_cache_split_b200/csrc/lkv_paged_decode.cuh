@@ -77,6 +77,8 @@ struct PagedSegment {
   int slot;                  // partial slot; -1 where the segment is the whole unit
 };
 
+__device__ __forceinline__ int paged_tiles_of(int L) { return L / kPagedTile + (L % kPagedTile != 0); }
+
 struct PagedCursor {
   long long t_begin, t_end, t0;  // t0: the first tile of unit (b, u)
   int b, u, produced;
@@ -84,7 +86,7 @@ struct PagedCursor {
   __device__ __forceinline__ bool next(const PagedDecodeParams& p, int rows, PagedSegment& s) {
     while (b < p.B && t0 < t_end) {
       const int L = max(0, __ldg(p.pages.seq_lens + b));
-      const int nt = (L + kPagedTile - 1) / kPagedTile;
+      const int nt = paged_tiles_of(L);
       const long long lo = t_begin > t0 ? t_begin - t0 : 0;
       const long long hi = t_end - t0 < nt ? t_end - t0 : nt;
       const int cb = b, cu = u;
@@ -112,7 +114,7 @@ struct PagedCursor {
 };
 
 __device__ __forceinline__ long long paged_tiles(const PagedDecodeParams& p, int b) {
-  return b < p.B ? (max(0, __ldg(p.pages.seq_lens + b)) + kPagedTile - 1) / kPagedTile : 0;
+  return b < p.B ? paged_tiles_of(max(0, __ldg(p.pages.seq_lens + b))) : 0;
 }
 
 // Start of range `range`; called by one full warp.

@@ -381,6 +381,116 @@ def test_decode_pages_shared_by_requests(L, gpu):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+# Pages against the copies: runs of 8 .. 128 rows within a page, or single rows; every width of group, few rows and many.
+@pytest.mark.parametrize("d,G,H,s_q,lens,page", [
+    (128, 8, 128, 1, [200, 9], 8), (128, 4, 128, 1, [130, 500], 24), (128, 7, 14, 1, [385], 40), (128, 2, 128, 1, [300], 96),
+    (128, 1, 16, 1, [129, 640], 128), (128, 3, 60, 2, [700, 256], 256), (128, 2, 24, 1, [1500], 1000), (128, 5, 5, 1, [300], 7),
+    (256, 2, 16, 1, [200, 9], 8), (256, 3, 60, 2, [130, 500], 24), (256, 4, 256, 1, [385], 40), (256, 1, 30, 1, [300, 77], 1),
+    (256, 2, 128, 1, [700, 256], 256), (256, 1, 8, 2, [260], 9), (512, 1, 20, 1, [300, 40], 8), (512, 2, 60, 2, [131], 5)])
+def test_decode_page_sizes(L, gpu, d, G, H, s_q, lens, page):
+    rng = np.random.default_rng(31)
+    pool, table = make_pool(rng, lens, G, d, page)
+    q, qr = queries(rng, len(lens), s_q, H, d)
+    out, lse = _decode(L, gpu, q, qr, pool, G, table, lens, 1 / math.sqrt(d + D_ROPE))
+    torch.cuda.synchronize()
+    assert L.check_device() == 0
+    check_decode(out, lse, paged.paged_decode(q, qr, pool, G, table, lens, 1 / math.sqrt(d + D_ROPE)), d, max(lens))
+
+
+@pytest.mark.parametrize("d,G,H,page", [(128, 2, 8, 8), (128, 2, 60, 3), (256, 2, 8, 16), (256, 2, 128, 5), (512, 1, 16, 16)])
+def test_decode_missing_pages_count_as_zero_rows(L, gpu, d, G, H, page):
+    rng = np.random.default_rng(32)
+    lens = [300, 140]
+    pool, table = make_pool(rng, lens, G, d, page)
+    q, qr = queries(rng, 2, 1, H, d)
+    broken, zeroed = table.copy(), pool.copy()
+    for k in (0, 1, 4, 140 // page):
+        broken[0, k] = -7 if k % 2 else pool.shape[0] + k
+        zeroed[table[0, k]] = 0
+        zeroed[table[0, k], :, :G * d // 2] = 0x88
+    out, lse = _decode(L, gpu, q, qr, pool, G, broken, lens, 0.05)
+    torch.cuda.synchronize()
+    assert L.check_device(clear=True) == L.SITE_BAD_ROW
+    check_decode(out, lse, paged.paged_decode(q, qr, zeroed, G, table, lens, 0.05), d, 300)
+
+
+@pytest.mark.parametrize("d,G,H", [(128, 2, 8), (256, 2, 40), (512, 1, 70)])
+def test_pool_with_rows_of_pages_side_by_side(L, gpu, d, G, H):
+    """Slot s of all pages side by side (rows further apart than pages): append and decode give what whole pages give."""
+    rng = np.random.default_rng(33)
+    lens, page, r = [90, 300], 16, G * d
+    pool, table = make_pool(rng, lens, G, d, page)
+    q, qr = queries(rng, 2, 1, H, d)
+    rows = torch.from_numpy(rng.standard_normal((6, r + 64)).astype(np.float32)).bfloat16().to(gpu)
+    whole = torch.from_numpy(pool).to(gpu)
+    side = torch.empty((page,) + (pool.shape[0], pool.shape[2]), dtype=torch.uint8, device=gpu).transpose(0, 1)
+    side.copy_(whole)
+    assert side.stride(0) < side.stride(1)
+    t, n = torch.from_numpy(table).to(gpu), torch.tensor(lens, dtype=torch.int32, device=gpu)
+    got = []
+    for place in (whole, side):
+        L.paged_append_int4(rows, place, r, t, n)
+        got.append(L.paged_decode_int4(q.to(gpu), qr.to(gpu), place, G, t, n, 0.06))
+    torch.cuda.synchronize()
+    assert L.check_device() == 0
+    assert torch.equal(whole, side)
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("d,G", [(128, 8), (256, 4), (512, 2)])
+def test_pool_past_32_bit_offsets(L, gpu, d, G):
+    """Pages more than 2^32 bytes into the pool: append and decode give what a small pool gives."""
+    rng = np.random.default_rng(34)
+    lens, page, r, H = [150, 33], 64, G * d, 8 * G
+    pool, table = make_pool(rng, lens, G, d, page)
+    q, qr = queries(rng, 2, 1, H, d)
+    rows = torch.from_numpy(rng.standard_normal((4, r + 64)).astype(np.float32)).bfloat16().to(gpu)
+    small, n = torch.from_numpy(pool).to(gpu), torch.tensor(lens, dtype=torch.int32, device=gpu)
+    first = -(-((1 << 32) + 12345) // (page * pool.shape[2]))
+    large = torch.empty((first + pool.shape[0], page, pool.shape[2]), dtype=torch.uint8, device=gpu)
+    large[first:].copy_(small)
+    got = []
+    for place, t in ((small, table), (large, np.where(table >= 0, table + first, table))):
+        t = torch.from_numpy(t.astype(np.int32)).to(gpu)
+        L.paged_append_int4(rows, place, r, t, n)
+        got.append(L.paged_decode_int4(q.to(gpu), qr.to(gpu), place, G, t, n, 0.06))
+    torch.cuda.synchronize()
+    assert L.check_device() == 0
+    assert torch.equal(large[first:], small)
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+def test_two_captured_graphs_replayed_in_turn(L, gpu):
+    """Two captured decodes, each with outputs and a workspace of its capture's own: replays in any order, and on two
+    streams at once, give what plain calls give."""
+    rng = np.random.default_rng(35)
+    cases = []
+    for d, G, H, lens, page in [(128, 4, 64, [2000, 70], 32), (256, 2, 64, [900, 1, 300], 64)]:
+        pool, table = make_pool(rng, lens, G, d, page)
+        q, qr = queries(rng, len(lens), 1, H, d)
+        args = (q.to(gpu), qr.to(gpu), torch.from_numpy(pool).to(gpu), G, torch.from_numpy(table).to(gpu),
+                torch.tensor(lens, dtype=torch.int32, device=gpu), 0.06)
+        want = L.paged_decode_int4(*args)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = L.paged_decode_int4(*args)
+        cases.append((graph, got, want, args))
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for order in ((0, 1), (1, 0), (0, 0), (1, 1)):
+        for _, got, _, _ in cases:
+            got[0].fill_(float("nan"))
+        torch.cuda.synchronize()
+        for s, k in zip((s1, s2) if order[0] != order[1] else (s1, s1), order):
+            with torch.cuda.stream(s):
+                cases[k][0].replay()
+        torch.cuda.synchronize()
+        for k in set(order):
+            _, got, want, _ = cases[k]
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert L.check_device() == 0
+
+
 def test_decode_runs_repeat_bit_for_bit_and_on_two_streams(L, gpu):
     rng = np.random.default_rng(25)
     d, G, H, lens, page = 128, 8, 128, [3000, 10, 900], 64

@@ -159,6 +159,19 @@ def test_rope_refusals(lkv_built):
     assert _rope(L, n=1 << 62, heads=1, d=64) == L.ERR_UNSUPPORTED
 
 
+def test_in_place_needs_the_same_strides(lkv_built):
+    """The same array with other strides would be written where other rows are still to be read."""
+    L = lkv_built
+    assert _append(L, held=GOOD, hs=584) == L.ERR_INVALID_ARG
+    assert _append(L, held=GOOD, hs=576, n=0) == L.OK
+    strides = dict(x=GOOD, xts=64 * 192, xhs=192, pos=GOOD, freqs=GOOD, n=8, heads=64, d=192, first=0, rot=64, inter=0, inv=0,
+                   gain=1.0, dtype=L.BF16, out=GOOD, ots=64 * 192, ohs=192)
+    assert L._rope(*dict(strides, ots=65 * 192).values(), None) == L.ERR_INVALID_ARG
+    assert L._rope(*dict(strides, ohs=200).values(), None) == L.ERR_INVALID_ARG
+    assert L._rope(*dict(strides, n=0).values(), None) == L.OK
+    assert L._rope(*dict(strides, heads=1 << 30).values(), None) == L.ERR_UNSUPPORTED
+
+
 def _append(L, **kw):
     a = dict(rows=GOOD, rs=576, n=8, pool=GOOD, ps=64 * 416, prs=416, pages=10, page=64, table=GOOD, ts=4, mp=4, lens=GOOD,
              cu=GOOD, batch=4, r=512, dr=64, freqs=GOOD, inter=0, gain=1.0, held=None, hs=0)
