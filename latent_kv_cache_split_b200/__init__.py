@@ -546,6 +546,13 @@ def _empty_on(stream, shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _empty_as(stream, t):
+    """A contiguous uninitialised tensor of t's shape and type (empty_like is the cheaper call)."""
+    if stream is None and t.is_contiguous():
+        return torch.empty_like(t)
+    return _empty_on(stream, t.shape, t.dtype, t.device)
+
+
 def _expect(t, dtype, name):
     if t.dtype != dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
@@ -591,7 +598,7 @@ def rope_rotate(x, positions, freqs, first=0, interleaved=False, inverse=False, 
     if len(shape) < 3 or x.stride(-1) != 1:
         raise ValueError("x must be [..., heads, d] with unit inner stride")
     if out is None:
-        out = _empty_on(stream, shape, dtype, x.device)
+        out = _empty_as(stream, x)
     elif out.shape != shape or out.stride(-1) != 1 or (out.data_ptr() == x.data_ptr() and out.stride() != x.stride()):
         raise ValueError("out must have x's shape and unit inner stride, and x's strides if it is x's memory")
     heads, d = shape[-2:]
@@ -716,7 +723,7 @@ def paged_decode_int4(q, q_rope, pool, groups, block_table, seq_lens, scale, out
     if rb == 0 or pool.shape[2] < rb:
         raise ValueError("unsupported groups * d / d_rope, or pool rows shorter than int4_cache_row_bytes(groups * d, d_rope)")
     if out is None:
-        out = _empty_on(stream, shape, torch.bfloat16, q.device)
+        out = _empty_as(stream, q)
     elif out.shape != shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
         raise ValueError("out must be contiguous bf16 of q's shape")
     if lse is None:
