@@ -115,23 +115,24 @@ lkv_status allow_smem(Kernel k, size_t bytes, bool (&ready)[kMaxDevices]) {
 
 // The decode kernel, then the combine as its programmatic dependent: its launch overlaps the decode, and its
 // blocks wait for the decode's completion before they read the partials.
-template <int D, int N>
+template <int D, int N, bool kTma>
 lkv_status launch_decode(const PagedDecodeParams& p, cudaStream_t s) {
+  using Cfg = PagedCfg<D, N, kTma>;
   static bool ready[kMaxDevices];
   lkv_status st;
-  if ((st = allow_smem(paged_decode_kernel<D, N>, PagedCfg<D, N>::kSmem, ready)) != LKV_OK) return st;
+  if ((st = allow_smem(paged_decode_kernel<D, N, kTma>, Cfg::kSmem, ready)) != LKV_OK) return st;
   PagedMaps maps = {};
-  if (PagedCfg<D, N>::kTma) {
+  if (kTma) {
     const Paged& g = p.pages;
     const uint64_t rb = row_bytes_of(p.G * D, 64), ps = g.n_pages > 1 ? g.page_stride : g.row_stride * g.page_size;
     auto map = [&](CUtensorMap* m, uint32_t bytes, CUtensorMapSwizzle sw) {
       return make_tmap_u8_3d(m, g.pool, rb, g.page_size, g.n_pages, g.row_stride, ps, bytes, p.box_rows, sw);
     };
-    if (!map(&maps.codes, D / 2, PagedCfg<D, N>::kWide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE) ||
+    if (!map(&maps.codes, D / 2, Cfg::kWide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE) ||
         !map(&maps.scales, 16, CU_TENSOR_MAP_SWIZZLE_NONE) || !map(&maps.keys, 128, CU_TENSOR_MAP_SWIZZLE_128B))
       return LKV_ERR_UNSUPPORTED;  // strides past what a tensor map holds
   }
-  paged_decode_kernel<D, N><<<p.P, kPagedThreads, PagedCfg<D, N>::kSmem, s>>>(p, maps);
+  paged_decode_kernel<D, N, kTma><<<p.P, kPagedThreads, Cfg::kSmem, s>>>(p, maps);
   if ((st = launched()) != LKV_OK) return st;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.P, (N + kPagedCombineWarps - 1) / kPagedCombineWarps);
@@ -147,10 +148,19 @@ lkv_status launch_decode(const PagedDecodeParams& p, cudaStream_t s) {
   return e == cudaSuccess ? st : LKV_ERR_CUDA;
 }
 
+// Tiles come by TMA where pages hold runs of enough rows: a copy costs about as much as 25 of its rows.  64 x 8192 tokens:
+// @RULE@
+template <int D>
+lkv_status launch_decode_of(const PagedDecodeParams& p, int N, cudaStream_t s) {
+  if constexpr (D <= 256) {
+    if (p.box_rows >= (D == 128 ? 32 : 16))
+      return N == 16 ? launch_decode<D, 16, true>(p, s) : N == 32 ? launch_decode<D, 32, true>(p, s) : launch_decode<D, 64, true>(p, s);
+  }
+  return N == 16 ? launch_decode<D, 16, false>(p, s) : N == 32 ? launch_decode<D, 32, false>(p, s) : launch_decode<D, 64, false>(p, s);
+}
+
 lkv_status launch_decode_for(const PagedDecodeParams& p, int d, int N, cudaStream_t s) {
-  if (d == 128) return N == 16 ? launch_decode<128, 16>(p, s) : N == 32 ? launch_decode<128, 32>(p, s) : launch_decode<128, 64>(p, s);
-  if (d == 256) return N == 16 ? launch_decode<256, 16>(p, s) : N == 32 ? launch_decode<256, 32>(p, s) : launch_decode<256, 64>(p, s);
-  return N == 16 ? launch_decode<512, 16>(p, s) : N == 32 ? launch_decode<512, 32>(p, s) : launch_decode<512, 64>(p, s);
+  return d == 128 ? launch_decode_of<128>(p, N, s) : d == 256 ? launch_decode_of<256>(p, N, s) : launch_decode_of<512>(p, N, s);
 }
 
 }  // namespace
@@ -310,8 +320,8 @@ lkv_status lkv_paged_decode_int4(const void* q, const void* q_rope, const void* 
   p.P = w.P;
   p.lockstep = w.lockstep;
   p.sl2 = scale * 1.4426950408889634f;
-  p.box_rows = page_size % 8 ? 1 : 8;
-  while (p.box_rows > 1 && p.box_rows < kPagedTile && page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
+  p.box_rows = 1;
+  while (p.box_rows < kPagedTile && page_size % (2 * p.box_rows) == 0) p.box_rows *= 2;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   p.seg_info = reinterpret_cast<int*>(ws + w.seg);

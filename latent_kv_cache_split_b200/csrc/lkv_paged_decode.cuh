@@ -54,7 +54,7 @@ struct PagedDecodeParams {
   float* part_o;       // [2P][N][D]
   int* err;
   unsigned long long wait_limit_ns;
-  int box_rows;  // rows of a copy: the largest power of two in the page size up to 128, or 1 where that is below 8
+  int box_rows;  // rows of a copy: the largest power of two in the page size, 128 at most
 };
 
 // The pool as three-dimensional tensors of bytes {row, page_size, n_pages} for the copies of a group's codes, of 16 bytes
@@ -160,8 +160,10 @@ __device__ __forceinline__ PagedCursor paged_locate(const PagedDecodeParams& p, 
 }
 
 // ------------------------------------------------------------------------------------------
-template <int D, int N>
+// kTma: codes, scales and RoPE keys come by TMA into a ring of raw tiles; else the converters load them themselves.
+template <int D, int N, bool kTma>
 struct PagedCfg {
+  static_assert(!kTma || D <= 256, "no shared memory for raw tiles");
   static constexpr int kBox = kPagedTile * 128;  // 128 keys x 64 bf16, 128-byte swizzle
   static constexpr int kVBoxes = D / 64;
   static constexpr int kVStage = kVBoxes * kBox;  // the state in shared memory: the value operand
@@ -169,16 +171,13 @@ struct PagedCfg {
   // A there, 32 cycles of its bandwidth; from TMEM it runs at the tensor core's rate, 16 cycles at N = 32), else from
   // the value operand's tile.
   static constexpr bool kTS = D <= 256;
-  // Codes, scales and RoPE keys come by TMA into a ring of raw tiles where shared memory has the room; at D = 512 the
-  // converters load them themselves.
-  static constexpr bool kTma = D <= 256;
   // QK reads the RoPE key from the raw tile (the copy leaves it as an MMA wants it) where the ring is deep enough to hold
   // the tile that long, else the converters put it into TMEM.
-  static constexpr bool kKeyRaw = D == 128;
-  static constexpr bool kWide = D == 256;  // codes in rows of 128 bytes, which the copy swizzles
+  static constexpr bool kKeyRaw = kTma && D == 128;
+  static constexpr bool kWide = kTma && D == 256;  // codes in rows of 128 bytes, which the copy swizzles
   // Converters: two groups that take turns at the tiles with 32 keys a warp, or one with 16 keys a warp of every tile.  A warp's
   // tile is a chain of waits, reads, stores and fences whose length hardly depends on the keys.
-  static constexpr int kTurns = D == 128 ? 2 : 1;
+  static constexpr int kTurns = kTma && D == 128 ? 2 : 1;
   static constexpr int kCW = kPagedConv / kTurns;  // warps of a group
   static constexpr int kKCols = (kTS ? D / 2 : 0) + (kKeyRaw ? 0 : 32);  // TMEM columns of a stage: the key operand
   static constexpr int kStages = D == 128 ? 3 : D == 256 ? 2 : 1;
@@ -195,7 +194,7 @@ struct PagedCfg {
   static constexpr int kGW = kPagedSoft / kGroups;  // warps of a group
   static constexpr int kRW = 4 * N / kGW;           // rows of a softmax warp
   static constexpr int kSBufs = D == 256 && N == 64 ? 1 : 2;  // S^T buffers
-  static constexpr int kPs = D >= 256 && N == 64 ? 1 : 2;     // P buffers
+  static constexpr int kPs = N == 64 && (D == 512 || (D == 256 && kTma)) ? 1 : 2;  // P buffers
   static constexpr int kQBox = N * 128;
   static constexpr int kQBytes = (kVBoxes + 1) * kQBox;
   static constexpr int kPBytes = kPagedTile * N * 2;
@@ -347,7 +346,7 @@ __device__ __forceinline__ void static_for(F&& f) {
 // A segment's Q as the K-major B operand, rows behind the group's last as zeros.  The columns follow what the converters
 // put into TMEM: register j of half h of a 128-column block is columns 32 (h + 2m) + 8e + 2i with j = 16m + 4e + i, of the
 // RoPE key 8 (h + 2m) + 2i with j = 4m + i, and a 16-byte piece p holds j = 2p and 2p + 1, each for h = 0 and 1.
-template <int D, int N>
+template <int D, int N, bool kTma>
 __device__ __noinline__ void paged_load_q(const PagedDecodeParams& p, const PagedSegment& s, uint8_t* qsm, int first, int step) {
   constexpr int kC = (D + 64) / 8;
 #pragma unroll 2
@@ -359,12 +358,12 @@ __device__ __noinline__ void paged_load_q(const PagedDecodeParams& p, const Page
       const int i = g >= p.hpg;
       const size_t qrow = (static_cast<size_t>(s.b) * p.s_q + i) * p.h_q + s.group * p.hpg + (g - i * p.hpg);
       const __nv_bfloat16* q = p.q + qrow * D;
-      if (piece >= D / 8 && PagedCfg<D, N>::kKeyRaw) {
+      if (piece >= D / 8 && PagedCfg<D, N, kTma>::kKeyRaw) {
         x = __ldg(reinterpret_cast<const uint4*>(p.q_rope + qrow * 64) + cc);
       } else if (piece >= D / 8) {
         const uint32_t* k = reinterpret_cast<const uint32_t*>(p.q_rope + qrow * 64) + 8 * (cc >> 1) + 2 * (cc & 1);
         x = make_uint4(__ldg(k), __ldg(k + 4), __ldg(k + 1), __ldg(k + 5));
-      } else if (PagedCfg<D, N>::kTS) {
+      } else if (PagedCfg<D, N, kTma>::kTS) {
         const int j = piece & 15;
         const uint32_t* k = reinterpret_cast<const uint32_t*>(q) + 64 * (piece >> 4) + 32 * (j >> 3) + 4 * ((j >> 1) & 3) + 2 * (j & 1);
         x = make_uint4(__ldg(k), __ldg(k + 16), __ldg(k + 1), __ldg(k + 17));
@@ -425,10 +424,10 @@ __device__ __noinline__ void paged_store_out(const PagedDecodeParams& p, const P
   }
 }
 
-template <int D, int N>
+template <int D, int N, bool kTma>
 __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __grid_constant__ PagedDecodeParams p,
                                                                            const __grid_constant__ PagedMaps maps) {
-  using Cfg = PagedCfg<D, N>;
+  using Cfg = PagedCfg<D, N, kTma>;
   constexpr int TN = kPagedTile, ST = Cfg::kStages, BL = Cfg::kBlocks, SS = Cfg::kSBufs, PS = Cfg::kPs;
   constexpr int RW = Cfg::kRW, MB = Cfg::kMB, NG = Cfg::kGroups, GW = Cfg::kGW;
   constexpr int kBox = Cfg::kBox;
@@ -436,7 +435,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
 
   extern __shared__ __align__(1024) uint8_t paged_smem_raw[];
   constexpr int RD = Cfg::kRaws;
-  __shared__ PagedSmem<RW, N, NG, Cfg::kTma ? 1 : kPagedConv, ST * BL, RD> sm;
+  __shared__ PagedSmem<RW, N, NG, kTma ? 1 : kPagedConv, ST * BL, RD> sm;
   static_assert(Cfg::kSmem + sizeof(sm) <= 232448, "shared memory budget");
   uint8_t* dsm = paged_smem_raw + ((1024u - (smem_u32(paged_smem_raw) & 1023u)) & 1023u);
   uint8_t* raw = dsm + ST * Cfg::kVStage;
@@ -581,10 +580,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
     }
   } else if (warp == 2) {
     // ================================================================== copies
-    // A tile's rows in boxes of box_rows within one page, lane i the boxes i, i + 32, ..; a box that lies behind the
-    // request's end or has no page is not copied.  Boxes of fewer than eight rows would break the 128-byte alignment
-    // that a tensor copy wants of codes and scales in shared memory: those go row by row as plain bulk copies.
-    if constexpr (Cfg::kTma) {
+    // A tile's rows in boxes of box_rows within one page, a lane a box; a box that lies behind the request's end or has no
+    // page is not copied.
+    if constexpr (kTma) {
       PagedCursor& walk = sm.walk[kPagedSoft];
       PagedSegment& seg = sm.conv_seg[0];
       if (lane == 0) walk = sm.cur;
@@ -625,55 +623,31 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
         const int odd = x.group & 1 ? PK_ODD_GROUP : 0;
         if (n >= RD) wait(sm.raw_free[rw], n / RD - 1, PW_RAWFREE);
         if (__any_sync(0xffffffffu, *const_cast<volatile uint32_t*>(&sm.abort) != 0)) break;
-        for (int i0 = 0; i0 * rows < TN; i0 += 32) {
-          const int at = (i0 + lane) * rows, first = x.t * TN + at;
-          if (i0 > 0) page = find(x, at, slot);
-          const bool token = at < TN && first < x.L;
-          if (token && (page < 0 || page >= p.pages.n_pages)) {
-            record_error(p.err, LKV_SITE_BAD_ROW);
-            page = -1;
-          }
-          // the keys' states, four to a word
-          const unsigned some = __ballot_sync(0xffffffffu, page >= 0);
-          if (rows > 1) {
-            const int state = (some >> (4 * lane / rows) & 1 ? PK_ROW : PK_NO_PAGE) | odd, left = x.L - x.t * TN - 4 * lane;
-            uint32_t w = 0;
+        const int at = lane * rows;
+        if (at < TN && x.t * TN + at < x.L && (page < 0 || page >= p.pages.n_pages)) {
+          record_error(p.err, LKV_SITE_BAD_ROW);
+          page = -1;
+        }
+        // the keys' states, four to a word
+        const unsigned some = __ballot_sync(0xffffffffu, page >= 0);
+        const int state = (some >> (4 * lane / rows) & 1 ? PK_ROW : PK_NO_PAGE) | odd, left = x.L - x.t * TN - 4 * lane;
+        uint32_t w = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w |= static_cast<uint32_t>(j < left ? state : PK_END) << (8 * j);
-            *reinterpret_cast<uint32_t*>(&sm.state[rw][4 * lane]) = w;
-          } else {
-            sm.state[rw][at] = !token ? PK_END : (page < 0 ? PK_NO_PAGE : PK_ROW) | odd;
-          }
-          // the barrier learns of these copies' bytes before they can land, and of the tile's last ones with the
-          // arrival that it waits for
-          const uint32_t bytes = __popc(some) * rows * (128 + D / 2 + 16);
-          __syncwarp();
-          if (lane == 0) {
-            if ((i0 + 32) * rows < TN)
-              mbar_expect_tx(bar, bytes);
-            else
-              mbar_arrive_expect_tx(bar, bytes);
-          }
-          __syncwarp();
-          if (page >= 0) {
-            const uint32_t codes = dst + kBox + at * (D / 2), scales = dst + kBox + Cfg::kCodeBytes + at * 16;
-            tma_load_3d(dst + at * 128, &maps.keys, bar, key_at, slot, page);
-            const uint8_t* row = p.pages.pool + page * p.pages.page_stride + slot * p.pages.row_stride;
-            if (rows > 1 || Cfg::kWide)
-              tma_load_3d(codes, &maps.codes, bar, code_at, slot, page);
-            else
-              bulk_load(codes, row + code_at, D / 2, bar);
-            if (rows > 1)
-              tma_load_3d(scales, &maps.scales, bar, scale_at, slot, page);
-            else
-              bulk_load(scales, row + scale_at, 16, bar);
-          }
+        for (int j = 0; j < 4; ++j) w |= static_cast<uint32_t>(j < left ? state : PK_END) << (8 * j);
+        *reinterpret_cast<uint32_t*>(&sm.state[rw][4 * lane]) = w;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(some) * rows * (128 + D / 2 + 16));
+        __syncwarp();
+        if (page >= 0) {
+          tma_load_3d(dst + at * 128, &maps.keys, bar, key_at, slot, page);
+          tma_load_3d(dst + kBox + at * (D / 2), &maps.codes, bar, code_at, slot, page);
+          tma_load_3d(dst + kBox + Cfg::kCodeBytes + at * 16, &maps.scales, bar, scale_at, slot, page);
         }
         x = y;
         page = page_y;
         slot = slot_y;
         // with a single raw tile its copies wait for the converters: the rows can come as far as L2 meanwhile (GLA-2: 265 -> 259 us)
-        if (RD == 1 && rows > 1 && page >= 0 && page < p.pages.n_pages) {
+        if (RD == 1 && page >= 0 && page < p.pages.n_pages) {
           tma_prefetch_3d(&maps.keys, key_at, slot, page);
           tma_prefetch_3d(&maps.codes, x.group * (D / 2), slot, page);
           tma_prefetch_3d(&maps.scales, r / 2 + (x.group * (D / 16) & ~15), slot, page);
@@ -755,7 +729,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
         }
       }
     };
-    if constexpr (Cfg::kTma) {
+    if constexpr (kTma) {
       const int tiles = static_cast<int>(sm.cur.t_end - sm.cur.t_begin);
       const int raw_row = key0 + paged_raw_row<Cfg::kWide>(rr), x8 = Cfg::kWide ? raw_row & 7 : 0;
       for (int n = turn; n < tiles; n += Cfg::kTurns) {
@@ -915,7 +889,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
       ++xc;
     };
     auto load_q = [&](const PagedSegment& s) {
-      paged_load_q<D, N>(p, s, qsm, (sw % GW) * 32 + lane, 32 * GW);
+      paged_load_q<D, N, kTma>(p, s, qsm, (sw % GW) * 32 + lane, 32 * GW);
       warp_arrive(sm.q_ready);
     };
 
