@@ -148,12 +148,14 @@ lkv_status launch_decode(const PagedDecodeParams& p, cudaStream_t s) {
   return e == cudaSuccess ? st : LKV_ERR_CUDA;
 }
 
-// Tiles come by TMA where pages hold runs of enough rows: a copy costs about as much as 25 of its rows.  64 x 8192 tokens:
-// @RULE@
+// Tiles come by TMA where pages hold runs of 16 rows: a copy costs about as much as 25 of its rows.  64 x 8192 tokens, by TMA
+// against loaded by the converters: 8 groups of 128, 32 rows, pages of 64 270 against 340 us, of 16 307 against 360 us, of
+// 48 320 against 342 us; 2 groups of 256, 64 rows, pages of 64 146 against 232 us, of 16 156 against 232 us; 4 groups, pages
+// of 16 266 against 323 us, of 8 351 against 327 us.
 template <int D>
 lkv_status launch_decode_of(const PagedDecodeParams& p, int N, cudaStream_t s) {
   if constexpr (D <= 256) {
-    if (p.box_rows >= (D == 128 ? 32 : 16))
+    if (p.box_rows >= 16)
       return N == 16 ? launch_decode<D, 16, true>(p, s) : N == 32 ? launch_decode<D, 32, true>(p, s) : launch_decode<D, 64, true>(p, s);
   }
   return N == 16 ? launch_decode<D, 16, false>(p, s) : N == 32 ? launch_decode<D, 32, false>(p, s) : launch_decode<D, 64, false>(p, s);

@@ -224,7 +224,7 @@ struct __align__(16) PagedSmem {
   alignas(16) uint8_t state[RD][kPagedTile];  // of a raw tile's keys: PagedKeyState
   uint32_t tmem_base, abort;
   // Walk state of the warps that run out of registers first: read where it is needed.
-  PagedCursor cur, walk[kPagedSoft + NC];  // NC: the converters, or the warp that copies for them
+  PagedCursor cur, walk[kPagedSoft + NC];  // NC: the converters, or the two warps that copy for them
   PagedSegment seg[kPagedSoft][2], conv_seg[NC];
 };
 
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
 
   extern __shared__ __align__(1024) uint8_t paged_smem_raw[];
   constexpr int RD = Cfg::kRaws;
-  __shared__ PagedSmem<RW, N, NG, kTma ? 1 : kPagedConv, ST * BL, RD> sm;
+  __shared__ PagedSmem<RW, N, NG, kTma ? 2 : kPagedConv, ST * BL, RD> sm;
   static_assert(Cfg::kSmem + sizeof(sm) <= 232448, "shared memory budget");
   uint8_t* dsm = paged_smem_raw + ((1024u - (smem_u32(paged_smem_raw) & 1023u)) & 1023u);
   uint8_t* raw = dsm + ST * Cfg::kVStage;
@@ -451,8 +451,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
       mbar_init(smem_u32(&sm.empty[s]), 1);
     }
     for (int s = 0; s < RD; ++s) {
-      mbar_init(smem_u32(&sm.raw_full[2 * s]), 1);
-      mbar_init(smem_u32(&sm.raw_full[2 * s + 1]), 1);
+      mbar_init(smem_u32(&sm.raw_full[2 * s]), 2);  // the two copying warps
+      mbar_init(smem_u32(&sm.raw_full[2 * s + 1]), 2);
       mbar_init(smem_u32(&sm.raw_free[s]), Cfg::kCW + Cfg::kKeyRaw);  // the converters' reads, and QK
     }
     for (int s = 0; s < 3; ++s) sm.vote[0][s] = sm.vote[1][s] = 0;
@@ -578,13 +578,14 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
       const WaitCtl dc{&zero, p.err, p.wait_limit_ns};
       mbar_wait(smem_u32(&sm.drain), 0, dc, kPagedSite + PW_DRAIN);
     }
-  } else if (warp == 2) {
+  } else if (warp < 4) {
     // ================================================================== copies
     // A tile's rows in boxes of box_rows within one page, a lane a box; a box that lies behind the request's end or has no
-    // page is not copied.
+    // page is not copied.  Warp 2 copies the RoPE keys, warp 3 codes and scales: the copies of a warp's lanes are issued
+    // one after the other, and their sum is on the way of every tile.
     if constexpr (kTma) {
-      PagedCursor& walk = sm.walk[kPagedSoft];
-      PagedSegment& seg = sm.conv_seg[0];
+      PagedCursor& walk = sm.walk[kPagedSoft + warp - 2];
+      PagedSegment& seg = sm.conv_seg[warp - 2];
       if (lane == 0) walk = sm.cur;
       struct Tile {
         int t, L, group;  // t < 0: none
@@ -599,58 +600,62 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
         }
         return Tile{walk_t++, seg.L, seg.group, p.pages.table + seg.b * p.pages.table_stride};
       };
-      // the page of the row `at` of a tile, -1 where there is none, and its slot there
-      auto find = [&](const Tile& x, int at, int& slot) -> int {
+      const int r = p.G * D, rows = p.box_rows, at = lane * rows;
+      const int key_at = int4_rope_at(r);
+      // the page of this lane's box of a tile, -1 where it holds no token or has none, and the box's slot there
+      auto find = [&](const Tile& x, int& slot) -> int {
         const int key = x.t * TN + at;
         if (x.t < 0 || at >= TN || key >= x.L) return -1;
         const int k = p.pages.page_shift >= 0 ? key >> p.pages.page_shift : key / p.pages.page_size;
         slot = key - k * p.pages.page_size;
         return k < p.pages.max_pages ? __ldg(x.table + k) : -1;
       };
-      const int r = p.G * D, rows = p.box_rows;
-      const int key_at = int4_rope_at(r);
       int n = 0, slot = 0;
       Tile x = next_tile();
-      int page = find(x, lane * rows, slot);
+      int page = find(x, slot);
       for (; x.t >= 0; ++n) {
         // the next tile's pages are asked for ahead of this one's wait
         const Tile y = next_tile();
         int slot_y = 0;
-        const int page_y = find(y, lane * rows, slot_y);
+        const int page_y = find(y, slot_y);
         const int rw = n % RD;
         const uint32_t bar = smem_u32(&raw_full(n)), dst = raw_base + rw * Cfg::kRawBytes;
         const int code_at = x.group * (D / 2), scale_at = r / 2 + (x.group * (D / 16) & ~15);
-        const int odd = x.group & 1 ? PK_ODD_GROUP : 0;
+        if (page >= p.pages.n_pages) page = -1;
+        const unsigned some = __ballot_sync(0xffffffffu, page >= 0);
+        uint32_t states = 0;  // of four keys
+        if (warp == 2) {
+          if (page < 0 && at < TN && x.t * TN + at < x.L) record_error(p.err, LKV_SITE_BAD_ROW);
+          const int state = (some >> (4 * lane / rows) & 1 ? PK_ROW : PK_NO_PAGE) | (x.group & 1 ? PK_ODD_GROUP : 0);
+          const int left = x.L - x.t * TN - 4 * lane;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) states |= static_cast<uint32_t>(j < left ? state : PK_END) << (8 * j);
+        }
         if (n >= RD) wait(sm.raw_free[rw], n / RD - 1, PW_RAWFREE);
         if (__any_sync(0xffffffffu, *const_cast<volatile uint32_t*>(&sm.abort) != 0)) break;
-        const int at = lane * rows;
-        if (at < TN && x.t * TN + at < x.L && (page < 0 || page >= p.pages.n_pages)) {
-          record_error(p.err, LKV_SITE_BAD_ROW);
-          page = -1;
-        }
-        // the keys' states, four to a word
-        const unsigned some = __ballot_sync(0xffffffffu, page >= 0);
-        const int state = (some >> (4 * lane / rows) & 1 ? PK_ROW : PK_NO_PAGE) | odd, left = x.L - x.t * TN - 4 * lane;
-        uint32_t w = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w |= static_cast<uint32_t>(j < left ? state : PK_END) << (8 * j);
-        *reinterpret_cast<uint32_t*>(&sm.state[rw][4 * lane]) = w;
+        if (warp == 2) *reinterpret_cast<uint32_t*>(&sm.state[rw][4 * lane]) = states;
         __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(some) * rows * (128 + D / 2 + 16));
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(some) * rows * (warp == 2 ? 128 : D / 2 + 16));
         __syncwarp();
         if (page >= 0) {
-          tma_load_3d(dst + at * 128, &maps.keys, bar, key_at, slot, page);
-          tma_load_3d(dst + kBox + at * (D / 2), &maps.codes, bar, code_at, slot, page);
-          tma_load_3d(dst + kBox + Cfg::kCodeBytes + at * 16, &maps.scales, bar, scale_at, slot, page);
+          if (warp == 2) {
+            tma_load_3d(dst + at * 128, &maps.keys, bar, key_at, slot, page);
+          } else {
+            tma_load_3d(dst + kBox + at * (D / 2), &maps.codes, bar, code_at, slot, page);
+            tma_load_3d(dst + kBox + Cfg::kCodeBytes + at * 16, &maps.scales, bar, scale_at, slot, page);
+          }
         }
         x = y;
         page = page_y;
         slot = slot_y;
-        // with a single raw tile its copies wait for the converters: the rows can come as far as L2 meanwhile (GLA-2: 265 -> 259 us)
+        // with a single raw tile its copies wait for the converters: the rows can come as far as L2 meanwhile (GLA-2: 276 -> 251 us)
         if (RD == 1 && page >= 0 && page < p.pages.n_pages) {
-          tma_prefetch_3d(&maps.keys, key_at, slot, page);
-          tma_prefetch_3d(&maps.codes, x.group * (D / 2), slot, page);
-          tma_prefetch_3d(&maps.scales, r / 2 + (x.group * (D / 16) & ~15), slot, page);
+          if (warp == 2) {
+            tma_prefetch_3d(&maps.keys, key_at, slot, page);
+          } else {
+            tma_prefetch_3d(&maps.codes, x.group * (D / 2), slot, page);
+            tma_prefetch_3d(&maps.scales, r / 2 + (x.group * (D / 16) & ~15), slot, page);
+          }
         }
       }
       // no copy may still be on its way when the block exits
