@@ -45,6 +45,7 @@ struct PagedDecodeParams {
   int RB;        // row blocks of a group
   int U;         // units of a request: G * RB
   int P;         // ranges (CTAs)
+  int unit_cost; // tiles that a unit's start and end count for
   int lockstep;  // the U units of a request run on neighbouring CTAs at the same pace
   float sl2;     // scale * log2(e)
   __nv_bfloat16* out;  // [B, s_q, h_q, D]
@@ -64,11 +65,11 @@ struct PagedMaps {
 };
 
 // ------------------------------------------------------------------------------------------
-// Work partition.  The tiles of all units are laid end to end (request-major) and cut into P equal
-// ranges; in lockstep the requests' tiles are cut into P / U blocks, and range p walks block p / U for
-// unit p % U, so that the units of a request read its RoPE keys and scales from L2.  A range is walked
-// as segments, the runs of its tiles that belong to one unit; a segment that is not a whole unit leaves
-// a partial (slot 0 the range's first segment, 1 its last).
+// Work partition.  The tiles of all units, and before a unit's first one the cost of the unit itself (its queries' load and its
+// result's store, as unit_cost tiles), are laid end to end (request-major) and cut into P equal ranges; in lockstep the
+// requests' are cut into P / U blocks, and range p walks block p / U for unit p % U, so that the units of a request read its RoPE
+// keys and scales from L2.  A range is walked as segments, the runs of its tiles that belong to one unit; a segment that is
+// not a whole unit leaves a partial (slot 0 the range's first segment, 1 its last).
 // ------------------------------------------------------------------------------------------
 struct PagedSegment {
   int b, unit, group, row0;  // unit = b * U + u; row0: the unit's first row in its group
@@ -80,17 +81,18 @@ struct PagedSegment {
 __device__ __forceinline__ int paged_tiles_of(int L) { return L / kPagedTile + (L % kPagedTile != 0); }
 
 struct PagedCursor {
-  long long t_begin, t_end, t0;  // t0: the first tile of unit (b, u)
+  long long t_begin, t_end, t0;  // t0: where unit (b, u) begins
   int b, u, produced;
 
   __device__ __forceinline__ bool next(const PagedDecodeParams& p, int rows, PagedSegment& s) {
     while (b < p.B && t0 < t_end) {
       const int L = max(0, __ldg(p.pages.seq_lens + b));
       const int nt = paged_tiles_of(L);
-      const long long lo = t_begin > t0 ? t_begin - t0 : 0;
-      const long long hi = t_end - t0 < nt ? t_end - t0 : nt;
+      const long long at = t0 + p.unit_cost;  // of the unit's first tile
+      const long long lo = t_begin > at ? t_begin - at : 0;
+      const long long hi = t_end - at < nt ? t_end - at : nt;
       const int cb = b, cu = u;
-      t0 += nt;
+      t0 += nt > 0 ? p.unit_cost + nt : 0;
       if (p.lockstep || ++u == p.U) {
         if (!p.lockstep) u = 0;
         ++b;
@@ -113,15 +115,17 @@ struct PagedCursor {
   }
 };
 
-__device__ __forceinline__ long long paged_tiles(const PagedDecodeParams& p, int b) {
-  return b < p.B ? paged_tiles_of(max(0, __ldg(p.pages.seq_lens + b))) : 0;
+// What a unit of request b counts for.
+__device__ __forceinline__ long long paged_cost(const PagedDecodeParams& p, int b) {
+  const int nt = b < p.B ? paged_tiles_of(max(0, __ldg(p.pages.seq_lens + b))) : 0;
+  return nt > 0 ? p.unit_cost + nt : 0;
 }
 
 // Start of range `range`; called by one full warp.
 __device__ __forceinline__ PagedCursor paged_locate(const PagedDecodeParams& p, int range, int lane) {
   const int mult = p.lockstep ? 1 : p.U;
   long long total = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) total += paged_tiles(p, b0 + lane);
+  for (int b0 = 0; b0 < p.B; b0 += 32) total += paged_cost(p, b0 + lane);
 #pragma unroll
   for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   total *= mult;
@@ -135,7 +139,7 @@ __device__ __forceinline__ PagedCursor paged_locate(const PagedDecodeParams& p, 
   c.t0 = total;
   long long acc = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const long long t = paged_tiles(p, b0 + lane) * mult;
+    const long long t = paged_cost(p, b0 + lane) * mult;
     long long incl = t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -223,6 +227,7 @@ struct __align__(16) PagedSmem {
   uint32_t vote[2][3];
   alignas(16) uint8_t state[RD][kPagedTile];  // of a raw tile's keys: PagedKeyState
   uint32_t tmem_base, abort;
+  int tiles;  // of the range
   // Walk state of the warps that run out of registers first: read where it is needed.
   PagedCursor cur, walk[kPagedSoft + NC];  // NC: the converters, or the two warps that copy for them
   PagedSegment seg[kPagedSoft][2], conv_seg[NC];
@@ -474,8 +479,14 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
     fence_mbar_init();
   }
   if (warp == 4) {
-    const PagedCursor c = paged_locate(p, range, lane);
-    if (lane == 0) sm.cur = c;
+    PagedCursor c = paged_locate(p, range, lane);
+    if (lane == 0) {
+      sm.cur = c;
+      PagedSegment s;
+      int tiles = 0;
+      while (c.next(p, N, s)) tiles += s.tile_hi - s.tile_lo;
+      sm.tiles = tiles;
+    }
   }
   if (warp == 0) {
     tmem_alloc(smem_u32(&sm.tmem_base), Cfg::kTmemCols);
@@ -735,7 +746,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
       }
     };
     if constexpr (kTma) {
-      const int tiles = static_cast<int>(sm.cur.t_end - sm.cur.t_begin);
+      const int tiles = sm.tiles;
       const int raw_row = key0 + paged_raw_row<Cfg::kWide>(rr), x8 = Cfg::kWide ? raw_row & 7 : 0;
       for (int n = turn; n < tiles; n += Cfg::kTurns) {
         const int rw = n % RD;
@@ -1093,32 +1104,33 @@ constexpr int kPagedMaxRanges = 1024;
 
 template <int D, int N>
 __global__ void __launch_bounds__(kPagedCombineWarps * 32) paged_combine_kernel(const __grid_constant__ PagedDecodeParams p) {
-  __shared__ int piece[kPagedMaxRanges];
+  __shared__ int info[2 * kPagedMaxRanges], piece[kPagedMaxRanges];
   __shared__ int n_pieces, unit;
   griddep_wait();  // a programmatic dependent of the decode kernel: its writes first
   const int range = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  const int2 own = *reinterpret_cast<const int2*>(p.seg_info + 2 * range);
+  const bool in0 = own.x >= 0 && (own.x & 3) == 1, in1 = own.y >= 0 && (own.y & 3) == 1;
+  if (!in0 && !in1) return;
+  // every range's entry at once: a walk from range to range would wait for each load in turn
+  for (int i = 2 * range + tid; i < 2 * p.P; i += blockDim.x) info[i] = p.seg_info[i];
+  __syncthreads();
   if (tid == 0) {
-    n_pieces = 0;
-    for (int slot = 0; slot < 2; ++slot) {
-      const int s = p.seg_info[2 * range + slot];
-      if (s < 0 || (s & 3) != 1) continue;
-      unit = s >> 2;
-      piece[0] = 2 * range + slot;
-      int n = 1;
-      const int step = p.lockstep ? p.U : 1;
-      for (int q = range + step; q < p.P; q += step) {
-        const int v = p.seg_info[2 * q];
-        if (v < 0) continue;  // a range without tiles
-        if ((v >> 2) != unit) break;
-        piece[n++] = 2 * q;
-        if (v & 2) break;
-      }
-      n_pieces = n;
+    const int slot = in1 ? 1 : 0;
+    unit = (slot ? own.y : own.x) >> 2;
+    piece[0] = 2 * range + slot;
+    int n = 1;
+    const int step = p.lockstep ? p.U : 1;
+    for (int q = range + step; q < p.P; q += step) {
+      const int v = info[2 * q];
+      if (v < 0) continue;  // a range without tiles
+      if ((v >> 2) != unit) break;
+      piece[n++] = 2 * q;
+      if (v & 2) break;
     }
+    n_pieces = n;
   }
   __syncthreads();
   const int n = n_pieces;
-  if (n == 0) return;
   const int row = blockIdx.y * kPagedCombineWarps + (tid >> 5);
   const int b = unit / p.U, u = unit - b * p.U, group = u / p.RB;
   const int g = (u - group * p.RB) * N + row;
@@ -1132,18 +1144,23 @@ __global__ void __launch_bounds__(kPagedCombineWarps * 32) paged_combine_kernel(
   float4 acc[D / 128];
 #pragma unroll
   for (int c = 0; c < D / 128; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-  for (int k = 0; k < n; ++k) {
-    const size_t at = static_cast<size_t>(piece[k]) * N + row;
-    const float w = expf(p.part_lse[at] - top);  // 0 for a piece whose keys the row does not see
-    tot += w;
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    // 0 for a piece whose keys the row does not see
+    const float wl = k0 + lane < n ? expf(p.part_lse[static_cast<size_t>(piece[k0 + lane]) * N + row] - top) : 0.f;
+    const int m = min(32, n - k0);
+#pragma unroll 4
+    for (int k = 0; k < m; ++k) {
+      const float w = __shfl_sync(0xffffffffu, wl, k);
+      const float* part = p.part_o + (static_cast<size_t>(piece[k0 + k]) * N + row) * D;
+      tot += w;
 #pragma unroll
-    for (int c = 0; c < D / 128; ++c) {
-      const float4 o = *reinterpret_cast<const float4*>(p.part_o + at * D + 128 * c + 4 * lane);
-      acc[c].x = fmaf(w, o.x, acc[c].x);
-      acc[c].y = fmaf(w, o.y, acc[c].y);
-      acc[c].z = fmaf(w, o.z, acc[c].z);
-      acc[c].w = fmaf(w, o.w, acc[c].w);
+      for (int c = 0; c < D / 128; ++c) {
+        const float4 o = *reinterpret_cast<const float4*>(part + 128 * c + 4 * lane);
+        acc[c].x = fmaf(w, o.x, acc[c].x);
+        acc[c].y = fmaf(w, o.y, acc[c].y);
+        acc[c].z = fmaf(w, o.z, acc[c].z);
+        acc[c].w = fmaf(w, o.w, acc[c].w);
+      }
     }
   }
   const float inv = tot == 0.f ? 0.f : 1.f / tot;
