@@ -687,7 +687,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
     const int r = p.G * D;
     const uint8_t* pool = p.pages.pool;
     const int key_at = int4_rope_at(r);
-    uint4 code[kHalves][kH][2], key[4];
+    constexpr int kHL = D == 512 ? 2 : kH;  // blocks of codes in registers: at D = 512 the others follow as these are used
+    uint4 code[kHalves][kHL][2], key[4];
+    const uint8_t* codes_at = nullptr;
     uint32_t scale[kHalves][2 * kH];  // of the chunks 2m and 2m + 1
     uint32_t mask = 0x000f000fu, magic = 0x43004300u;
     asm volatile("" : "+r"(mask), "+r"(magic));
@@ -698,7 +700,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
     for (int e = 0; e < 4; ++e) at_word[e] = vrow * 128 + (((4 * hf + e) ^ (vrow & 7)) << 4);
     const uint32_t tlane = tbase + K0 + (static_cast<uint32_t>(key0) << 16);
 #pragma unroll
-    for (int h = 0; h < kH; ++h) code[0][h][0] = code[0][h][1] = make_uint4(0u, 0u, 0u, 0u);
+    for (int h = 0; h < kHL; ++h) code[0][h][0] = code[0][h][1] = make_uint4(0u, 0u, 0u, 0u);
     // one tile's registers to the value operand and, where QK wants it there, to TMEM
     auto convert = [&](int n) {
       const int st = n % ST;
@@ -725,7 +727,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
           const uint32_t s2 = __byte_perm(scale[half][2 * h + m], 0, pick);
           const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&s2);
           const __nv_bfloat162 o = __hmul2(s, __float2bfloat162_rn(-136.f));
-          const uint32_t word[4] = {code[half][h][m].x, code[half][h][m].y, code[half][h][m].z, code[half][h][m].w};
+          const uint32_t word[4] = {code[half][h % kHL][m].x, code[half][h % kHL][m].y, code[half][h % kHL][m].z, code[half][h % kHL][m].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint4 x = int4_expand(word[e], mask, magic, s, o);
@@ -742,6 +744,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
           fence_proxy_async_smem();  // ahead of the next global loads: its memory barrier would wait for them
           tc_fence_before();
           warp_arrive(sm.full[st * BL + (BL > 1 ? h : 0)]);
+        }
+        if (kHL < kH && h + kHL < kH && codes_at) {
+          code[half][h % kHL][0] = ldg16<0>(codes_at + 64 * (h + kHL));
+          code[half][h % kHL][1] = ldg16<32>(codes_at + 64 * (h + kHL));
         }
       }
     };
@@ -840,7 +846,8 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
         const uint8_t* sp = pool + at + (r / 2 + group * (D / 16));
         const uint8_t* kp = pool + at + (16 * hf + key_at);
         if (__all_sync(0xffffffffu, at >= 0) || at >= 0) {
-          static_for<kH>([&](auto h) {
+          codes_at = cp;
+          static_for<kHL>([&](auto h) {
             code[0][h][0] = ldg16<64 * h>(cp);
             code[0][h][1] = ldg16<64 * h + 32>(cp);
           });
@@ -855,6 +862,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
           }
           static_for<4>([&](auto m) { key[m] = ldg16<32 * m>(kp); });
         } else {  // no token: scales of 0 make any codes zeros, and the key is zeros
+          codes_at = nullptr;
 #pragma unroll
           for (int m = 0; m < 2 * kH; ++m) scale[0][m] = 0;
 #pragma unroll
