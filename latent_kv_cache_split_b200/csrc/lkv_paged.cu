@@ -149,9 +149,9 @@ lkv_status launch_decode(const PagedDecodeParams& p, cudaStream_t s) {
 }
 
 // Tiles come by TMA where pages hold runs of 16 rows: a copy costs about as much as 25 of its rows.  64 x 8192 tokens, by TMA
-// against loaded by the converters: 8 groups of 128, 32 rows, pages of 64 270 against 340 us, of 16 307 against 360 us, of
-// 48 320 against 342 us; 2 groups of 256, 64 rows, pages of 64 146 against 232 us, of 16 156 against 232 us; 4 groups, pages
-// of 16 266 against 323 us, of 8 351 against 327 us.
+// against loaded by the converters: 8 groups of 128, 32 rows, pages of 64 269 against 338 us, of 16 309 against 357 us; 2 groups
+// of 256, 64 rows, pages of 64 145 against 224 us, of 16 155 against 224 us; 4 groups, 32 rows, pages of 16 258 against 264
+// us, of 8 354 against 264 us.
 template <int D>
 lkv_status launch_decode_of(const PagedDecodeParams& p, int N, cudaStream_t s) {
   if constexpr (D <= 256) {

@@ -260,13 +260,9 @@ __device__ __noinline__ void paged_wait_slow(uint32_t bar, uint32_t parity, vola
   }
 }
 
-// Key k's row in the value tile and in P^T: bits 1, 2, 3 of k move to 2, 3, 1.  The lanes that expand keys g and g + 8
-// then write different 16-byte columns of the swizzled rows.  (Where the value tile is the key operand too, its rows are
-// the lanes of S^T, and stay.)
-template <bool kTS>
-__device__ __forceinline__ int paged_key_row(int k) {
-  return kTS ? (k & ~14) | ((k >> 2) & 2) | ((k & 6) << 1) : k;
-}
+// Key k's row in the value tile and in P^T where K is in TMEM: bits 1, 2, 3 of k move to 2, 3, 1.  The lanes that expand
+// keys g and g + 8 then write different 16-byte columns of the swizzled rows.
+__device__ __forceinline__ int paged_key_row(int k) { return (k & ~14) | ((k >> 2) & 2) | ((k & 6) << 1); }
 
 // The raw tile's row of the key in TMEM lane k: where the converters read 128-byte rows of codes and of RoPE keys, bits 0, 1, 2,
 // 3 of k move to 1, 0, 3, 2, so that eight neighbouring lanes read eight different 16-byte columns of the swizzled rows.
@@ -687,14 +683,17 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
     const int r = p.G * D;
     const uint8_t* pool = p.pages.pool;
     const int key_at = int4_rope_at(r);
-    constexpr int kHL = D == 512 ? 2 : kH;  // blocks of codes in registers: at D = 512 the others follow as these are used
+    constexpr int kHL = kTma ? kH : 1;  // blocks of codes in registers: where they are loaded here, the next follows as one is used
     uint4 code[kHalves][kHL][2], key[4];
     const uint8_t* codes_at = nullptr;
     uint32_t scale[kHalves][2 * kH];  // of the chunks 2m and 2m + 1
     uint32_t mask = 0x000f000fu, magic = 0x43004300u;
     asm volatile("" : "+r"(mask), "+r"(magic));
     const uint32_t pick = hf ? 0x3232u : 0x1010u;  // this lane's scale of a pair, twice
-    const int vrow = key0 + paged_key_row<Cfg::kTS>(rr);
+    // (D = 512) V's rows are QK's too, so a key keeps its row, and the lanes take the keys of the codes in an order that writes
+    // different columns of the swizzled rows (MLA 195 -> 183 us)
+    const int rc = Cfg::kTS ? rr : 2 * (lane >> 2) + (lane & 1);
+    const int vrow = key0 + (Cfg::kTS ? paged_key_row(rr) : rc);
     uint32_t at_word[4];  // where word e of this lane's chunk goes in the value tile
 #pragma unroll
     for (int e = 0; e < 4; ++e) at_word[e] = vrow * 128 + (((4 * hf + e) ^ (vrow & 7)) << 4);
@@ -841,11 +840,12 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
         return off;
       };
       auto load_rows = [&](long long off, int group) {
-        const long long at = __shfl_sync(0xffffffffu, off, rr);
+        const long long at = __shfl_sync(0xffffffffu, off, rc), key_from = Cfg::kTS ? at : __shfl_sync(0xffffffffu, off, rr);
         const uint8_t* cp = pool + at + (16 * hf + group * (D / 2));
         const uint8_t* sp = pool + at + (r / 2 + group * (D / 16));
-        const uint8_t* kp = pool + at + (16 * hf + key_at);
-        if (__all_sync(0xffffffffu, at >= 0) || at >= 0) {
+        const uint8_t* kp = pool + key_from + (16 * hf + key_at);
+        const bool whole = __all_sync(0xffffffffu, at >= 0 && key_from >= 0);
+        if (whole || at >= 0) {
           codes_at = cp;
           static_for<kHL>([&](auto h) {
             code[0][h][0] = ldg16<64 * h>(cp);
@@ -860,11 +860,14 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
               scale[0][4 * h] = v.x, scale[0][4 * h + 1] = v.y, scale[0][4 * h + 2] = v.z, scale[0][4 * h + 3] = v.w;
             });
           }
-          static_for<4>([&](auto m) { key[m] = ldg16<32 * m>(kp); });
         } else {  // no token: scales of 0 make any codes zeros, and the key is zeros
           codes_at = nullptr;
 #pragma unroll
           for (int m = 0; m < 2 * kH; ++m) scale[0][m] = 0;
+        }
+        if (whole || key_from >= 0) {
+          static_for<4>([&](auto m) { key[m] = ldg16<32 * m>(kp); });
+        } else {
 #pragma unroll
           for (int m = 0; m < 4; ++m) key[m] = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -927,7 +930,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
     }
 
     // where this key's weights go: 2N bytes a key, 16-byte chunk c at c ^ the swizzle of that width
-    const int krow = paged_key_row<Cfg::kTS>(k);
+    const int krow = Cfg::kTS ? paged_key_row(k) : k;
     const int x8 = N == 64 ? (krow & 7) : N == 32 ? ((krow >> 1) & 3) : ((krow >> 2) & 1);
     uint8_t* prow0 = psm + krow * (2 * N);
     PagedCursor& walk = sm.walk[sw];
