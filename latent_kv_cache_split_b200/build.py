@@ -20,7 +20,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "liblkv.so")
 SOURCES = ["lkv_api.cu", "lkv_proj.cu", "lkv_fp8.cu", "lkv_paged.cu"]
-HEADERS = ["lkv_ptx.cuh", "lkv_sched.cuh", "lkv_decode_tc.cuh", "lkv_decode_swap.cuh", "lkv_decode_swap_wide.cuh", "lkv_mla_pair.cuh", "lkv_gemm.cuh", "lkv_aux.cuh", "lkv_tma_host.h", "lkv_rope.cuh", "lkv_int4.cuh", "lkv_paged_decode.cuh"]
+HEADERS = ["lkv_ptx.cuh", "lkv_sched.cuh", "lkv_decode_tc.cuh", "lkv_decode_swap.cuh", "lkv_decode_swap_wide.cuh", "lkv_mla_pair.cuh", "lkv_gemm.cuh", "lkv_aux.cuh", "lkv_tma_host.h", "lkv_rope.cuh", "lkv_int4.cuh", "lkv_paged_ptx.cuh", "lkv_paged_decode.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -5,28 +5,35 @@
 // products are taken with the keys in the MMA's M dimension, since a unit has few rows:
 //   S^T[key, row] = K[key, :] . Q[row, :]          M = 128 keys, N rows, K = D + 64 columns
 //   O^T[c, row]  += V^T[c, key] . P^T[key, row]    M = 128 value columns (D / 128 blocks), N rows, K = 128 keys
-// A 128-key tile costs (D + 64) / 16 + D / 16 MMAs, and at N <= 64 each takes about 46 cycles to issue
-// whatever N is (measured with one issuing thread; 40 with two), so rows come almost free up to 64.
+// A 128-key tile costs (D + 64) / 16 + D / 16 MMAs.  With K in tensor memory one takes 16 cycles at N = 32 and 32 at N = 64,
+// with both operands in shared memory, as PV's are, 40 and 48 (it reads 4 KB of A): some 570 cycles a tile of the 2000 that
+// one takes at D = 128, N = 32.
 //
-// 4-bit codes are no operand of these MMAs, so converter warps turn each tile into bf16 in shared
-// memory, exactly: (word >> 4i) & 0x000f000f | 0x43004300 is a pair of bf16 128 + u, and one fma by the
-// scale s with -136 s (17 x 4 bits: exact) leaves (u - 8) s.  Rows without a token become zeros, so
-// nothing behind a request's end reaches an MMA.
+// 4-bit codes are no operand of these MMAs, so converter warps turn each tile into bf16, exactly: (word >> 4i) & 0x000f000f |
+// 0x43004300 is a pair of bf16 128 + u, and one fma by the scale s with -136 s (17 x 4 bits: exact) leaves (u - 8) s.  A key
+// behind the request's end or without a page gets scales of 0, so that nothing of it reaches PV; the scores behind the end are
+// masked, and the RoPE key of a token without a page is zeros.
 //
 // Softmax in the exp2 domain against a reference per row instead of the running maximum: the first
 // tile's maximum, raised only when some score passes it by 2^64 (fp32 sums and bf16 weights have the
 // range, and a weight's relative precision does not depend on it).  A tile then needs no reduction over
 // its keys, only a vote of the softmax warps on whether any score passed.
 //
-// Warps: 0 QK issuer and TMEM owner, 1 PV issuer, from 4 on softmax and epilogue (warp w: TMEM lane quadrant
-// w % 4; a thread owns one key of the tile, or one value column of O^T), then the converters, in groups
-// that take turns at the tiles.
+// Warps: 0 QK issuer and TMEM owner, 1 PV issuer, 2 and 3 the copies of codes, scales and RoPE keys (idle where the
+// converters load for themselves), 4 to 19 softmax and epilogue (warp w: TMEM lane quadrant w % 4; a thread owns one key of
+// the tile, or one value column of O^T), 20 to 27 converters.
+//
+// What bounds it is neither bytes nor FLOPs but the length of a tile's way through these warps against the tiles that shared
+// memory holds: from the copy to PV's end a tile takes about 8000 cycles (of them 1500 for the copy, 1000 for the conversion, 2400
+// for the softmax), with three to six tiles on the way.  64 requests of 8192 tokens: 8 groups of 128 with 32 rows 270 us (1.40
+// TB/s, 318 TFLOP/s), MLA's 512 columns with 128 rows at half the length 182 us (401 TFLOP/s: a single stage, so conversion and
+// products alternate); 8 of 131072 with 2 groups of 256, 64 rows, 235 us (1.86 TB/s, 658 TFLOP/s).
 #pragma once
 #include <cstdint>
 #include <utility>
 #include <cuda_bf16.h>
 #include "lkv_int4.cuh"
-#include "lkv_ptx.cuh"
+#include "lkv_paged_ptx.cuh"
 
 namespace lkv {
 
@@ -180,13 +187,13 @@ struct PagedCfg {
   static constexpr bool kKeyRaw = kTma && D == 128;
   static constexpr bool kWide = kTma && D == 256;  // codes in rows of 128 bytes, which the copy swizzles
   // Converters: two groups that take turns at the tiles with 32 keys a warp, or one with 16 keys a warp of every tile.  A warp's
-  // tile is a chain of waits, reads, stores and fences whose length hardly depends on the keys.
+  // tile is a chain of waits, reads, stores and fences whose length hardly depends on the keys (GTA 273 -> 270 us).
   static constexpr int kTurns = kTma && D == 128 ? 2 : 1;
   static constexpr int kCW = kPagedConv / kTurns;  // warps of a group
   static constexpr int kKCols = (kTS ? D / 2 : 0) + (kKeyRaw ? 0 : 32);  // TMEM columns of a stage: the key operand
   static constexpr int kStages = D == 128 ? 3 : D == 256 ? 2 : 1;
   // Stages are handed on in blocks of 128 columns: QK starts on the first columns while the rest is converted, and the next
-  // tile's conversion while PV runs over the last columns (GLA-2 263 -> 252 us, MLA 224 -> 218 us).
+  // tile's conversion while PV runs over the last columns (GLA-2 251 -> 234 us, MLA 224 -> 218 us).
   static constexpr int kBlocks = D / 128;
   static constexpr int kRaws = !kTma ? 1 : D == 256 ? (N == 16 ? 2 : 1) : N == 64 ? 2 : 3;  // raw tiles
   static constexpr int kCodeBytes = kPagedTile * (D / 2), kScaleBytes = kPagedTile * 16;
@@ -655,7 +662,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
         x = y;
         page = page_y;
         slot = slot_y;
-        // with a single raw tile its copies wait for the converters: the rows can come as far as L2 meanwhile (GLA-2: 276 -> 251 us)
+        // with a single raw tile its copies wait for the converters: the rows can come as far as L2 meanwhile (GLA-2 238 -> 234 us)
         if (RD == 1 && page >= 0 && page < p.pages.n_pages) {
           if (warp == 2) {
             tma_prefetch_3d(&maps.keys, key_at, slot, page);
