@@ -375,6 +375,7 @@ lkv_status lkv_paged_append_int4(const void* new_rows, int64_t new_row_stride, i
  * Strides of the pool below 2^40 bytes (LKV_ERR_UNSUPPORTED).
  * workspace_bytes >= lkv_paged_decode_workspace_size(...) (host-only, no CUDA call; 0 on bad input).
  * Calls that may run at the same time (other streams, captured graphs) need workspaces of their own.
+ * out, lse and the workspace overlap no other argument's memory.
  */
 size_t lkv_paged_decode_workspace_size(int batch, int s_q, int h_q, int groups, int d, int num_sms);
 lkv_status lkv_paged_decode_int4(const void* q, const void* q_rope, const void* pool,

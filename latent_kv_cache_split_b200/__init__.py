@@ -537,20 +537,20 @@ def _call(where: str, index: int, stream, f, *args):
         raise LkvError(status, where)
 
 
-def _empty_on(stream, shape, dtype, device):
-    """An uninitialised tensor for a call on `stream`: from that stream's pool, so that a workspace freed at the call's
-    return is not handed to another stream while the kernels run."""
+def _empty_on(stream, shape, dtype, ref):
+    """An uninitialised tensor on ref's GPU for a call on `stream`: from that stream's pool, so that a workspace freed at the
+    call's return is not handed to another stream while the kernels run."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return ref.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return ref.new_empty(shape, dtype=dtype)
 
 
 def _empty_as(stream, t):
     """A contiguous uninitialised tensor of t's shape and type (empty_like is the cheaper call)."""
     if stream is None and t.is_contiguous():
         return torch.empty_like(t)
-    return _empty_on(stream, t.shape, t.dtype, t.device)
+    return _empty_on(stream, t.shape, t.dtype, t)
 
 
 def _expect(t, dtype, name):
@@ -727,11 +727,11 @@ def paged_decode_int4(q, q_rope, pool, groups, block_table, seq_lens, scale, out
     elif out.shape != shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
         raise ValueError("out must be contiguous bf16 of q's shape")
     if lse is None:
-        lse = _empty_on(stream, shape[:-1], torch.float32, q.device)
+        lse = _empty_on(stream, shape[:-1], torch.float32, q)
     elif lse.shape != shape[:-1] or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be contiguous [batch, s_q, h_q] fp32")
     if workspace is None:
-        workspace = _empty_on(stream, _paged_ws_on(index, B, s_q, h_q, groups, d), torch.uint8, q.device)
+        workspace = _empty_on(stream, _paged_ws_on(index, B, s_q, h_q, groups, d), torch.uint8, q)
     if not q.is_contiguous() or not q_rope.is_contiguous() or not workspace.is_contiguous():
         raise ValueError("query and workspace tensors must be contiguous")
     _call("lkv_paged_decode_int4", index, stream, _paged_decode, q.data_ptr(), q_rope.data_ptr(), *args, B, s_q, h_q,
