@@ -30,6 +30,7 @@
 // products alternate); 8 of 131072 with 2 groups of 256, 64 rows, 235 us (1.86 TB/s, 658 TFLOP/s).
 #pragma once
 #include <cstdint>
+#include <type_traits>
 #include <utility>
 #include <cuda_bf16.h>
 #include "lkv_int4.cuh"
@@ -195,6 +196,9 @@ struct PagedCfg {
   // Stages are handed on in blocks of 128 columns: QK starts on the first columns while the rest is converted, and the next
   // tile's conversion while PV runs over the last columns (GLA-2 251 -> 234 us, MLA 224 -> 218 us).
   static constexpr int kBlocks = D / 128;
+  // K and V of a tile in two passes over its codes: K's TMEM is free once QK is done, long before PV leaves V's shared memory, so
+  // that the next tile's QK and softmax do not wait for it (GTA 270 -> 252 us, GLA-2 234 -> 232 us).
+  static constexpr bool kSplit = kTma;
   static constexpr int kRaws = !kTma ? 1 : D == 256 ? (N == 16 ? 2 : 1) : N == 64 ? 2 : 3;  // raw tiles
   static constexpr int kCodeBytes = kPagedTile * (D / 2), kScaleBytes = kPagedTile * 16;
   static constexpr int kRawBytes = kTma ? kBox + kCodeBytes + kScaleBytes : 0;  // RoPE keys, codes, scales
@@ -218,11 +222,11 @@ struct PagedCfg {
 };
 
 constexpr int kPagedSite = LKV_SITE_WAIT_BASE + 300;  // wait sites of this kernel
-enum PagedWaitSite { PW_EMPTY = 1, PW_RAW, PW_RAWFREE, PW_FULL, PW_SFREE, PW_QREADY, PW_PFULL, PW_OFREE, PW_SFULL, PW_ODONE, PW_VOTE, PW_XCHG, PW_FIN, PW_DRAIN };
+enum PagedWaitSite { PW_EMPTY = 1, PW_RAW, PW_RAWFREE, PW_FULL, PW_VFULL, PW_KFREE, PW_SFREE, PW_QREADY, PW_PFULL, PW_OFREE, PW_SFULL, PW_ODONE, PW_VOTE, PW_XCHG, PW_FIN, PW_DRAIN };
 
 template <int RW, int N, int NG, int NC, int FULL, int RD>
 struct __align__(16) PagedSmem {
-  uint64_t full[FULL], empty[FULL];  // of a stage's block
+  uint64_t full[FULL], v_full[FULL], empty[FULL], k_free[3];  // of a stage's block; of a stage
   uint64_t raw_full[2 * RD], raw_free[RD];  // two a raw tile, for its uses in turn: a group may wait a use ahead of the other's
   uint64_t s_full[2], s_free[2], p_full[2], o_done[2];
   uint64_t vote_bar[2], xchg_bar[2];  // of a softmax group
@@ -456,6 +460,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
   if (tid == 0) {
     for (int s = 0; s < ST * BL; ++s) {
       mbar_init(smem_u32(&sm.full[s]), Cfg::kCW);
+      mbar_init(smem_u32(&sm.v_full[s]), Cfg::kCW);
       mbar_init(smem_u32(&sm.empty[s]), 1);
     }
     for (int s = 0; s < RD; ++s) {
@@ -463,7 +468,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
       mbar_init(smem_u32(&sm.raw_full[2 * s + 1]), 2);
       mbar_init(smem_u32(&sm.raw_free[s]), Cfg::kCW + Cfg::kKeyRaw);  // the converters' reads, and QK
     }
-    for (int s = 0; s < 3; ++s) sm.vote[0][s] = sm.vote[1][s] = 0;
+    for (int s = 0; s < 3; ++s) {
+      mbar_init(smem_u32(&sm.k_free[s]), 1);
+      sm.vote[0][s] = sm.vote[1][s] = 0;
+    }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&sm.s_full[b]), 1);
       mbar_init(smem_u32(&sm.s_free[b]), GW);
@@ -554,6 +562,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
               }
             }
             if (Cfg::kKeyRaw) umma_commit(smem_u32(&sm.raw_free[rw]));
+            if (Cfg::kSplit) umma_commit(smem_u32(&sm.k_free[st]));
             umma_commit(smem_u32(&sm.s_full[sb]));
           }
         }
@@ -575,6 +584,10 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
             const uint64_t pdesc = N == 64 ? sdesc_sw128(paddr, 16, atom) : N == 32 ? sdesc_sw64(paddr, 16, atom) : sdesc_sw32(paddr, 16, atom);
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
+              if (Cfg::kSplit) {
+                wait(sm.v_full[st * BL + mb], n / ST, PW_VFULL);
+                tc_fence_after();
+              }
               const uint64_t vdesc = sdesc_sw128(v_base + st * Cfg::kVStage + 2 * mb * kBox, kBox, 1024);
 #pragma unroll
               for (int kk = 0; kk < TN / 16; ++kk)
@@ -707,14 +720,20 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
     const uint32_t tlane = tbase + K0 + (static_cast<uint32_t>(key0) << 16);
 #pragma unroll
     for (int h = 0; h < kHL; ++h) code[0][h][0] = code[0][h][1] = make_uint4(0u, 0u, 0u, 0u);
-    // one tile's registers to the value operand and, where QK wants it there, to TMEM
-    auto convert = [&](int n) {
+    // one tile's registers to the value operand (V) and, where QK wants it there, to TMEM (K), in one pass or in two
+    auto pass = [&](auto to_k, auto to_v, int n) {
+      constexpr bool kK = decltype(to_k)::value, kV = decltype(to_v)::value;
       const int st = n % ST;
-      if (n >= ST) wait(sm.empty[st * BL], n / ST - 1, PW_EMPTY);
-      tc_fence_after();
       uint8_t* stage = dsm + st * Cfg::kVStage;
       const uint32_t ktm = tlane + st * Cfg::kKCols;
-      if constexpr (!Cfg::kKeyRaw) {
+      if (n >= ST) {
+        if (kV)
+          wait(sm.empty[st * BL], n / ST - 1, PW_EMPTY);
+        else
+          wait(sm.k_free[st], n / ST - 1, PW_KFREE);
+      }
+      tc_fence_after();
+      if constexpr (kK && !Cfg::kKeyRaw) {
         uint32_t out[16];
 #pragma unroll
         for (int m = 0; m < 4; ++m) out[4 * m] = key[m].x, out[4 * m + 1] = key[m].y, out[4 * m + 2] = key[m].z, out[4 * m + 3] = key[m].w;
@@ -723,7 +742,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
 #pragma unroll
       for (int u = 0; u < kHalves * kH; ++u) {
         const int h = u % kH, half = u / kH;  // 128 columns of 16 keys
-        if (BL > 1 && h > 0 && n >= ST) {
+        if (kV && BL > 1 && h > 0 && n >= ST) {
           wait(sm.empty[st * BL + h], n / ST - 1, PW_EMPTY);
           tc_fence_after();
         }
@@ -733,28 +752,43 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
           const uint32_t s2 = __byte_perm(scale[half][2 * h + m], 0, pick);
           const __nv_bfloat162 s = *reinterpret_cast<const __nv_bfloat162*>(&s2);
           const __nv_bfloat162 o = __hmul2(s, __float2bfloat162_rn(-136.f));
-          const uint32_t word[4] = {code[half][h % kHL][m].x, code[half][h % kHL][m].y, code[half][h % kHL][m].z, code[half][h % kHL][m].w};
+          const uint4 c = code[half][h % kHL][m];
+          const uint32_t word[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint4 x = int4_expand(word[e], mask, magic, s, o);
-            *reinterpret_cast<uint4*>(stage + at_word[e] + half * 2048 + (2 * h + m) * kBox) = x;
+            if (kV) *reinterpret_cast<uint4*>(stage + at_word[e] + half * 2048 + (2 * h + m) * kBox) = x;
             out[4 * e] = x.x;
             out[4 * e + 1] = x.y;
             out[4 * e + 2] = x.z;
             out[4 * e + 3] = x.w;
           }
-          if (Cfg::kTS) tmem_st_16x64_x16(ktm + (half << 20) + 64 * h + 32 * m, out);
+          if (kK && Cfg::kTS) tmem_st_16x64_x16(ktm + (half << 20) + 64 * h + 32 * m, out);
         }
         if (BL > 1 || u == kHalves * kH - 1) {
-          if (Cfg::kTS || h == 0) tmem_wait_st();
-          fence_proxy_async_smem();  // ahead of the next global loads: its memory barrier would wait for them
+          if (kK && (Cfg::kTS || h == 0)) tmem_wait_st();
+          if (kV) fence_proxy_async_smem();  // ahead of the next global loads: its memory barrier would wait for them
           tc_fence_before();
-          warp_arrive(sm.full[st * BL + (BL > 1 ? h : 0)]);
+          warp_arrive((kK ? sm.full : sm.v_full)[st * BL + (BL > 1 ? h : 0)]);
         }
         if (kHL < kH && h + kHL < kH && codes_at) {
           code[half][h % kHL][0] = ldg16<0>(codes_at + 64 * (h + kHL));
           code[half][h % kHL][1] = ldg16<32>(codes_at + 64 * (h + kHL));
         }
+      }
+    };
+    auto convert = [&](int n) {
+      if constexpr (Cfg::kSplit) {
+        pass(std::true_type{}, std::false_type{}, n);
+        // opaque to the compiler, which would keep the first pass's values for the second one, in local memory
+#pragma unroll
+        for (int u = 0; u < kHalves * kHL * 2; ++u) {
+          uint4& c = code[u / (2 * kHL)][u / 2 % kHL][u & 1];
+          asm volatile("" : "+r"(c.x), "+r"(c.y), "+r"(c.z), "+r"(c.w));
+        }
+        pass(std::false_type{}, std::true_type{}, n);
+      } else {
+        pass(std::true_type{}, std::true_type{}, n);
       }
     };
     if constexpr (kTma) {
@@ -798,6 +832,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
                 else
                   key[m] = make_uint4(0u, 0u, 0u, 0u);
               }
+              if constexpr (Cfg::kKeyRaw) fence_proxy_async_smem();
             }
           }
         }
