@@ -6,7 +6,7 @@
 //   S^T[key, row] = K[key, :] . Q[row, :]          M = 128 keys, N rows, K = D + 64 columns
 //   O^T[c, row]  += V^T[c, key] . P^T[key, row]    M = 128 value columns (D / 128 blocks), N rows, K = 128 keys
 // A 128-key tile costs (D + 64) / 16 + D / 16 MMAs.  With K in tensor memory one takes 16 cycles at N = 32 and 32 at N = 64,
-// with both operands in shared memory, as PV's are, 40 and 48 (it reads 4 KB of A): some 570 cycles a tile of the 2000 that
+// with both operands in shared memory, as PV's are, 40 and 48 (it reads 4 KB of A): some 570 cycles a tile of the 1900 that
 // one takes at D = 128, N = 32.
 //
 // 4-bit codes are no operand of these MMAs, so converter warps turn each tile into bf16, exactly: (word >> 4i) & 0x000f000f |
@@ -25,9 +25,9 @@
 //
 // What bounds it is neither bytes nor FLOPs but the length of a tile's way through these warps against the tiles that shared
 // memory holds: from the copy to PV's end a tile takes about 8000 cycles (of them 1500 for the copy, 1000 for the conversion, 2400
-// for the softmax), with three to six tiles on the way.  64 requests of 8192 tokens: 8 groups of 128 with 32 rows 270 us (1.40
-// TB/s, 318 TFLOP/s), MLA's 512 columns with 128 rows at half the length 182 us (401 TFLOP/s: a single stage, so conversion and
-// products alternate); 8 of 131072 with 2 groups of 256, 64 rows, 235 us (1.86 TB/s, 658 TFLOP/s).
+// for the softmax), with three to six tiles on the way.  64 requests of 8192 tokens: 8 groups of 128 with 32 rows 252 us (1.50
+// TB/s, 340 TFLOP/s), MLA's 512 columns with 128 rows at half the length 182 us (400 TFLOP/s: a single stage, so conversion and
+// products alternate); 8 of 131072 with 2 groups of 256, 64 rows, 229 us (1.91 TB/s, 674 TFLOP/s).
 #pragma once
 #include <cstdint>
 #include <type_traits>
@@ -193,9 +193,10 @@ struct PagedCfg {
   static constexpr int kCW = kPagedConv / kTurns;  // warps of a group
   static constexpr int kKCols = (kTS ? D / 2 : 0) + (kKeyRaw ? 0 : 32);  // TMEM columns of a stage: the key operand
   static constexpr int kStages = D == 128 ? 3 : D == 256 ? 2 : 1;
-  // Stages are handed on in blocks of 128 columns: QK starts on the first columns while the rest is converted, and the next
-  // tile's conversion while PV runs over the last columns (GLA-2 251 -> 234 us, MLA 224 -> 218 us).
-  static constexpr int kBlocks = D / 128;
+  // Where a tile is converted in one pass, stages are handed on in blocks of 128 columns: QK starts on the first columns while the
+  // rest is converted, and the next tile's conversion while PV runs over the last columns (MLA 224 -> 218 us).  In two passes
+  // the barriers cost more than that gives (each some 200 cycles of a converter's way; GLA-2 232 us with blocks, 229 us without).
+  static constexpr int kBlocks = kTma ? 1 : D / 128;
   // K and V of a tile in two passes over its codes: K's TMEM is free once QK is done, long before PV leaves V's shared memory, so
   // that the next tile's QK and softmax do not wait for it (GTA 270 -> 252 us, GLA-2 234 -> 232 us).
   static constexpr bool kSplit = kTma;
@@ -584,8 +585,9 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
             const uint64_t pdesc = N == 64 ? sdesc_sw128(paddr, 16, atom) : N == 32 ? sdesc_sw64(paddr, 16, atom) : sdesc_sw32(paddr, 16, atom);
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
-              if (Cfg::kSplit) {
-                wait(sm.v_full[st * BL + mb], n / ST, PW_VFULL);
+              constexpr int kOf = MB / BL;  // M blocks of a stage's block
+              if (Cfg::kSplit && mb % kOf == 0) {
+                wait(sm.v_full[st * BL + mb / kOf], n / ST, PW_VFULL);
                 tc_fence_after();
               }
               const uint64_t vdesc = sdesc_sw128(v_base + st * Cfg::kVStage + 2 * mb * kBox, kBox, 1024);
