@@ -69,8 +69,8 @@ void launch_rope(const RopeParams& p, bool interleaved, dim3 blocks, dim3 thread
 
 // Rows of a unit (the MMA's N): the smallest of 16, 32, 64 that holds a group's rows, so that small groups
 // spend no softmax on padding; 64 at most, and a group of more rows is several units that read the same tiles.
-// 64 x 8192 tokens, 8 groups of 128: 16 rows 221 us as units of 16 and 264 us as units of 32, 32 rows 270 us
-// as units of 32 and 355 us as units of 64.
+// 64 x 8192 tokens, 8 groups of 128: 16 rows 222 us as units of 16 and 248 us as units of 32, 32 rows 252 us
+// as units of 32 and 370 us as units of 64.
 int paged_rows(int R) { return R <= 16 ? 16 : R <= 32 ? 32 : 64; }
 
 struct PagedPlan {
@@ -83,8 +83,8 @@ void paged_plan(PagedPlan* w, int s_q, int h_q, int groups, int d, int num_sms) 
   w->N = paged_rows(R);
   w->RB = (R + w->N - 1) / w->N;
   w->U = groups * w->RB;
-  // Units in lockstep share a request's RoPE keys and scales through L2 (64 x 8192 tokens, 8 groups of 32 rows: 270 us
-  // against 293 us); not where that leaves more than a tenth of the SMs without a range, nor for so few units that
+  // Units in lockstep share a request's RoPE keys and scales through L2 (64 x 8192 tokens, 8 groups of 32 rows: 252 us
+  // against 278 us); not where that leaves more than a tenth of the SMs without a range, nor for so few units that
   // there is little to share.
   const int sms = num_sms < kPagedMaxRanges ? num_sms : kPagedMaxRanges;
   const int whole = w->U <= sms ? sms / w->U * w->U : 0;
@@ -149,9 +149,9 @@ lkv_status launch_decode(const PagedDecodeParams& p, cudaStream_t s) {
 }
 
 // Tiles come by TMA where pages hold runs of 16 rows: a copy costs about as much as 25 of its rows.  64 x 8192 tokens, by TMA
-// against loaded by the converters: 8 groups of 128, 32 rows, pages of 64 269 against 338 us, of 16 309 against 357 us; 2 groups
-// of 256, 64 rows, pages of 64 145 against 224 us, of 16 155 against 224 us; 4 groups, 32 rows, pages of 16 258 against 264
-// us, of 8 354 against 264 us.
+// against loaded by the converters: 8 groups of 128, 32 rows, pages of 64 252 against 339 us, of 16 318 against 357 us; 2 groups
+// of 256, 64 rows, pages of 64 142 against 223 us, of 16 161 against 224 us; 4 groups, 32 rows, pages of 16 260 against 265
+// us, of 8 367 against 263 us.
 template <int D>
 lkv_status launch_decode_of(const PagedDecodeParams& p, int N, cudaStream_t s) {
   if constexpr (D <= 256) {
