@@ -286,9 +286,8 @@ __device__ __forceinline__ int paged_raw_row(int k) {
 template <int RW>
 __device__ __forceinline__ void tmem_load_rows(uint32_t taddr, float (&v)[RW]) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
-  if constexpr (RW == 32) {
-    tmem_ld32(taddr, reinterpret_cast<uint32_t(&)[32]>(*r));
-  } else if constexpr (RW == 16) {
+  static_assert(RW == 16 || RW == 8, "rows of a softmax warp");
+  if constexpr (RW == 16) {
     tmem_ld16(taddr, reinterpret_cast<uint32_t(&)[16]>(*r));
   } else {
     tmem_ld8(taddr, reinterpret_cast<uint32_t(&)[8]>(*r));
@@ -297,9 +296,7 @@ __device__ __forceinline__ void tmem_load_rows(uint32_t taddr, float (&v)[RW]) {
 template <int RW>
 __device__ __forceinline__ void tmem_store_rows(uint32_t taddr, const float (&v)[RW]) {
   const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
-  if constexpr (RW == 32) {
-    tmem_st32(taddr, reinterpret_cast<const uint32_t(&)[32]>(*r));
-  } else if constexpr (RW == 16) {
+  if constexpr (RW == 16) {
     tmem_st16(taddr, reinterpret_cast<const uint32_t(&)[16]>(*r));
   } else {
     tmem_st8(taddr, reinterpret_cast<const uint32_t(&)[8]>(*r));
