@@ -14,10 +14,12 @@
 // behind the request's end or without a page gets scales of 0, so that nothing of it reaches PV; the scores behind the end are
 // masked, and the RoPE key of a token without a page is zeros.
 //
-// Softmax in the exp2 domain against a reference per row instead of the running maximum: the first
-// tile's maximum, raised only when some score passes it by 2^64 (fp32 sums and bf16 weights have the
-// range, and a weight's relative precision does not depend on it).  A tile then needs no reduction over
-// its keys, only a vote of the softmax warps on whether any score passed.
+// Softmax in the exp2 domain against a reference per row instead of the running maximum: 16 above the
+// first tile's maximum, raised only when some score passes it by 8, so by 24 the maximum it was set to
+// (log2 units; a weight's relative precision does not depend on it).  Weights of a row's largest score
+// so far lie between 2^-16 and 2^8: a sum of 2^20 of them times values below 2^100, as the cache may
+// hold, stays below fp32's 2^128, and the least values, 2^-102, keep their place above 2^-126.  A tile
+// then needs no reduction over its keys, only a vote of the softmax warps on whether any score passed.
 //
 // Warps: 0 QK issuer and TMEM owner, 1 PV issuer, 2 and 3 the copies of codes, scales and RoPE keys (idle where the
 // converters load for themselves), 4 to 19 softmax and epilogue (warp w: TMEM lane quadrant w % 4; a thread owns one key of
@@ -42,7 +44,8 @@ constexpr int kPagedConv = 8;                          // converter warps
 constexpr int kPagedSoft = 16;                         // softmax warps
 constexpr int kPagedThreads = 32 * (4 + kPagedSoft + kPagedConv);  // issuers, softmax, converters
 constexpr int kPagedTile = 128;
-constexpr float kPagedRaise = 64.f;  // log2 units a score may pass its row's reference by
+constexpr float kPagedShift = 16.f;  // log2 units from a tile's maximum to the reference that it sets
+constexpr float kPagedRaise = 8.f;   // log2 units a score may pass its row's reference by
 
 struct PagedDecodeParams {
   Paged pages;
@@ -1044,7 +1047,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
           }
           float all[4];
           exchange(mw, all);
-          const float mt = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3]));
+          const float mt = fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3])) + kPagedShift;
           // a row that sees no key of the group's first tile sees none of its later ones: its reference stays 0
           const float up = first ? (mt == -INFINITY ? 0.f : mt) : fmaxf(mt, 0.f);
           m_run = first ? up : m_run + up;

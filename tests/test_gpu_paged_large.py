@@ -122,6 +122,28 @@ def test_references_rise_within_a_segment(L, gpu, d, G, H, s_q, page, kind):
     check_decode(out, lse, decode64(q, qr, pool, G, table, lens, scale), d, max(lens), kind)
 
 
+@pytest.mark.parametrize("step", [12, 36, 48, 1536])
+@pytest.mark.parametrize("exponent", [93, -105])
+@pytest.mark.parametrize("d,G,H,s_q,page", [(128, 4, 64, 1, 16), (128, 2, 128, 1, 1), (256, 2, 48, 1, 128), (512, 1, 128, 1, 64)])
+def test_values_over_the_cache_s_whole_range(L, gpu, d, G, H, s_q, page, exponent, step):
+    """Latents up to 105 2^93, just below 2^100, and scales from 8 2^-105 on, where scores rise by 12 to 1500 and more log2
+    units between tiles: sums of weights times values stay finite and keep their precision.  The latent columns of the queries
+    are 0, so the scores come from the RoPE keys."""
+    lens = _long(gpu, G, H, s_q)
+    pool, table = make_large(lens, G, d, page, H + step, gpu, exponent=exponent,
+                             key0=lambda b, t: torch.where(t // 128 % 4 == 2, float(step), 0.0))
+    q, qr = make_queries(len(lens), s_q, H, d, H, gpu)
+    q.zero_()
+    qr[..., 0] = 16.0
+    scale = 1 / math.sqrt(d + D_ROPE)
+    out, lse = L.paged_decode_int4(q, qr, pool, G, table, torch.tensor(lens, dtype=torch.int32, device=gpu), scale)
+    torch.cuda.synchronize()
+    assert L.check_device() == 0
+    ref = decode64(q, qr, pool, G, table, lens, scale)
+    back = 2.0 ** (-6 - exponent)      # exact: values as a cache with scales from 8 2^-6 on has them
+    check_decode(out.double() * back, lse, (ref[0] * back, ref[1], ref[2] * back, ref[3]), d, max(lens), f"{exponent} {step}")
+
+
 @pytest.mark.parametrize("d,G,H,s_q,page", [(128, 8, 128, 2, 64), (128, 2, 128, 1, 1), (256, 2, 128, 1, 16), (512, 1, 128, 2, 64)])
 def test_every_slot_idle(L, gpu, d, G, H, s_q, page):
     """As in the warm-up of a captured step: zeros and -inf, no table entry read; the captured call then serves requests."""
