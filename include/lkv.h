@@ -329,7 +329,8 @@ lkv_status lkv_rope_rotate(const void* x, int64_t x_token_stride, int64_t x_head
  *   then         d_rope bf16 values: the (rotated) RoPE key
  * The latent held is code * scale, exact in bf16: a scale is the smallest number of 4 significant bits
  * with 7 scale >= amax (amax the largest magnitude of the 32 columns); it is 0, with every code 0,
- * where amax < 2^-100.  code = x / scale rounded to the nearest integer, ties to even.
+ * where amax < 2^-100.  code = x / scale rounded to the nearest integer, ties to even.  32 columns with a
+ * NaN or an infinity among them are held as NaN: their scale is NaN, and their codes mean nothing.
  * lkv_int4_cache_row_bytes returns 0 unless r is a multiple of 32 in [32, 1024] and d_rope a multiple of
  * 8 in [0, 1024] (host-only, no CUDA call).
  */
@@ -344,7 +345,7 @@ size_t lkv_int4_cache_row_bytes(int r, int d_rope);
  *
  * Append: rotate, quantise and place the new rows.
  *   new_rows  [n_new, r + d_rope] bf16 (latent, then the RoPE key), row stride a multiple of 8 elements,
- *             16-byte aligned; values finite and below 2^100 in magnitude
+ *             16-byte aligned; magnitudes below 2^100, or NaN or infinite
  *   cu_new    [batch + 1] int32, device: rows cu_new[b] .. cu_new[b+1] - 1 are the newest of request b
  *             (rows from cu_new[batch] on are ignored); NULL: n_new / batch rows for every request
  *   freqs     [d_rope / 2] fp64 with `interleaved` and `gain` as above: the key is rotated to its
@@ -370,7 +371,9 @@ lkv_status lkv_paged_append_int4(const void* new_rows, int64_t new_row_stride, i
  *   out [batch, s_q, h_q, d] bf16, lse [batch, s_q, h_q] fp32
  * Query i sees tokens 0 .. seq_lens[b] - s_q + i; one that sees none (an idle slot, or the older query
  * of a one-token request) gets out = 0 and lse = -inf.  A token without a page counts as a row of zeros
- * and is recorded as LKV_SITE_BAD_ROW.  Rows behind a request's last token are not read as values.
+ * and is recorded as LKV_SITE_BAD_ROW.  Rows behind a request's last token are not read as values.  A
+ * latent held as NaN makes out and lse of its group's queries that see the token NaN, and the columns
+ * held as NaN in out of the group's older query, which does not; other groups and requests keep theirs.
  * Implemented: d 128, 256 or 512, groups * d <= 1024, d_rope = 64, s_q 1 or 2, s_q * h_q / groups <= 256.
  * Strides of the pool below 2^40 bytes (LKV_ERR_UNSUPPORTED).
  * workspace_bytes >= lkv_paged_decode_workspace_size(...) (host-only, no CUDA call; 0 on bad input).

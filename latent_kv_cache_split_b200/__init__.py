@@ -658,7 +658,8 @@ def paged_append_int4(new_rows, pool, r, block_table, seq_lens, cu_new=None, fre
     >= int4_cache_row_bytes(r, d_rope)] uint8, the key rotated to its position on the way (freqs and gain of
     rope_frequencies; freqs=None: stored as it comes).  seq_lens [batch] int32 counts each request's tokens, the new
     ones among them; rows cu_new[b] .. cu_new[b + 1] - 1 are the newest of request b (cu_new=None: n / batch each).
-    rows_out: gets the values the cache now holds (bf16, new_rows' shape; may be new_rows).  Returns pool."""
+    rows_out: gets the values the cache now holds (bf16, new_rows' shape; may be new_rows).  Latents below 2^100 in
+    magnitude; 32 columns with a NaN or an infinity among them are held as NaN.  Returns pool."""
     if new_rows.dtype != torch.bfloat16:
         raise TypeError("paged_append_int4 takes bf16 rows")
     args, B = _pool_args("paged_append_int4", pool, block_table, seq_lens)

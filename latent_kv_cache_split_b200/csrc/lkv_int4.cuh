@@ -75,6 +75,13 @@ struct AppendParams {
   int* err;
 };
 
+// The larger value, NaN where either is (fmaxf passes over NaN).
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 constexpr int kAppendThreads = 256;
 
 // Request of new row w: the last b with cu[b] <= w, its rows [begin, end) and its token count.  One step looks at 32
@@ -108,7 +115,8 @@ __device__ __forceinline__ int request_of(const int* cu, const int* seq_lens, in
 // bits and s = n 2^k with n in 8 .. 15, so x / s is a tie or at least 1/1920 away from one.  fma(x, 1 / s,
 // 1536) rounds x / s (off by under 2^-20) to a multiple of 2^-13, which puts ties back on the tie and
 // moves nothing else across one; adding 12582920 - 1536 then rounds to an integer, and leaves code + 8 in
-// the low bits of the sum's pattern.
+// the low bits of the sum's pattern.  A block with a NaN or an infinity gets a NaN for its scale, whatever
+// its codes (78k rows of 576: 35.8 -> 36.2 us for the maximum that keeps NaN).
 __global__ void __launch_bounds__(kAppendThreads) append_int4_kernel(const AppendParams p) {
   const int lane = threadIdx.x & 31;
   const long long w = (static_cast<long long>(blockIdx.x) * kAppendThreads + threadIdx.x) >> 5;
@@ -166,16 +174,18 @@ __global__ void __launch_bounds__(kAppendThreads) append_int4_kernel(const Appen
     for (int e = 0; e < 4; ++e) {
       x[2 * e] = __uint_as_float(word[e] << 16);
       x[2 * e + 1] = __uint_as_float(word[e] & 0xffff0000u);
-      amax = fmaxf(amax, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
+      amax = max_or_nan(amax, max_or_nan(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
     }
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    amax = max_or_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = max_or_nan(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     // amax = m 2^(e - 134) with m in 128 .. 255; the least n with 7 n 2 >= m, or else with 7 n 4 >= m
     const uint32_t bits = __float_as_uint(amax);
     const int m = static_cast<int>((bits >> 16) & 0x7fu) | 0x80, e = static_cast<int>(bits >> 23);
     const bool low = m <= 210;
     const int n = low ? (m + 13) / 14 : (m + 27) / 28;
-    const float s = e >= 27 ? static_cast<float>(n) * __uint_as_float(static_cast<uint32_t>(e - (low ? 6 : 5)) << 23) : 0.f;
+    // 0 below 2^-100, NaN where amax is infinite or none
+    const float s = static_cast<uint32_t>(e - 27) < 228u ? static_cast<float>(n) * __uint_as_float(static_cast<uint32_t>(e - (low ? 6 : 5)) << 23)
+                                                         : amax * 0.f;
     const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
     uint32_t code = 0u - (0x4b400000u + (0x4b400000u << 4) + (0x4b400000u << 8));  // the sums' patterns above their low bits
 #pragma unroll
