@@ -564,19 +564,22 @@ def rope_frequencies(rot: int, base: float = 10000.0, factor: float = 1.0, conte
 
     freqs[i] = base^(-2i / rot).  With factor > 1, for a context `factor` times the `context` that was trained
     on: a pair that turns more than beta_fast times over `context` keeps its frequency, one that turns less than
-    beta_slow times has it divided by factor, with a linear ramp between; gain = 1 + 0.1 ln factor.
-    beta_fast = inf divides every frequency (linear interpolation of the positions)."""
+    beta_slow times has it divided by factor, with a ramp between that is linear in the turns (a model trained with
+    a ramp over the pairs' numbers needs frequencies of its own); gain = 1 + 0.1 ln factor.
+    beta_fast = inf divides every frequency, with gain 1 (linear interpolation of the positions)."""
     if rot <= 0 or rot % 2 or not base > 0 or not factor >= 1 or context <= 0 or not 0 <= beta_slow < beta_fast:
         raise ValueError("rope_frequencies: rot even and positive, base > 0, factor >= 1, context > 0, "
                          "0 <= beta_slow < beta_fast")
     f = float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
     gain = 1.0
     if factor > 1:
-        turns = context * f / (2 * math.pi)
-        keep = (turns - beta_slow) / (beta_fast - beta_slow) if math.isfinite(beta_fast) else torch.zeros_like(f)
-        keep = keep.clamp(0.0, 1.0)
-        f = f * (keep + (1.0 - keep) / factor)
-        gain = 1.0 + 0.1 * math.log(factor)
+        if math.isfinite(beta_fast):
+            turns = context * f / (2 * math.pi)
+            keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
+            f = f * (keep + (1.0 - keep) / factor)
+            gain = 1.0 + 0.1 * math.log(factor)
+        else:
+            f = f / factor
     return f.to(device), gain
 
 

@@ -1,0 +1,12 @@
+"""What the documentation of the rotary and paged entry points promises beside the results, without a GPU."""
+import math
+
+import torch
+
+
+def test_interpolation_of_the_positions_has_gain_one(lkv_built):
+    """beta_fast = inf divides every frequency, which is the plain map at positions divided by factor: no gain."""
+    f, gain = lkv_built.rope_frequencies(64, factor=4.0, beta_fast=math.inf)
+    plain, _ = lkv_built.rope_frequencies(64)
+    assert torch.allclose(f, plain / 4, rtol=1e-15) and gain == 1.0
+    assert lkv_built.rope_frequencies(64, factor=4.0)[1] == 1.0 + 0.1 * math.log(4.0)
