@@ -39,7 +39,7 @@ lkv_status check_pool(Paged* g, const void* pool, int64_t page_stride, int64_t r
   const size_t rb = row_bytes_of(r, d_rope);
   if (!pool || !table || !seq_lens || rb == 0 || batch <= 0 || n_pages <= 0 || page_size <= 0 || max_pages <= 0)
     return LKV_ERR_INVALID_ARG;
-  if (!al(pool, 16) || page_stride % 16 || row_stride % 16 || row_stride < static_cast<int64_t>(rb) ||
+  if (!al(pool, 16) || !al(table, 4) || !al(seq_lens, 4) || page_stride % 16 || row_stride % 16 || row_stride < static_cast<int64_t>(rb) ||
       table_stride < max_pages)
     return LKV_ERR_INVALID_ARG;
   // pages do not overlap: whole pages apart, or their rows interleaved with others' (a view of a wider pool)
@@ -179,7 +179,7 @@ lkv_status lkv_rope_rotate(const void* x, int64_t x_token_stride, int64_t x_head
   if (x == out && (x_token_stride != out_token_stride || x_head_stride != out_head_stride)) return LKV_ERR_INVALID_ARG;
   if (rot / 2 > kRopeMaxPairs || heads > 1 << 20) return LKV_ERR_UNSUPPORTED;
   const int size = dtype == LKV_BF16 ? 2 : 4, wide = 16 / size;
-  if (!al(x, size) || !al(out, size) || !al(freqs, 8)) return LKV_ERR_INVALID_ARG;
+  if (!al(x, size) || !al(out, size) || !al(positions, 4) || !al(freqs, 8)) return LKV_ERR_INVALID_ARG;
   if (n_tok == 0) return LKV_OK;
   RopeParams p;
   p.x = x;
@@ -250,7 +250,7 @@ lkv_status lkv_paged_append_int4(const void* new_rows, int64_t new_row_stride, i
                              table_stride, max_pages, seq_lens, batch, r, d_rope);
   if (st != LKV_OK) return st;
   if (!new_rows || n_new < 0 || !al(new_rows, 16) || new_row_stride % 8 || new_row_stride < r + d_rope) return LKV_ERR_INVALID_ARG;
-  if (!cu_new && n_new % batch) return LKV_ERR_INVALID_ARG;
+  if (cu_new ? !al(cu_new, 4) : n_new % batch != 0) return LKV_ERR_INVALID_ARG;
   if (freqs && (!al(freqs, 8) || !finite_positive(gain))) return LKV_ERR_INVALID_ARG;
   if (rows_out && (!al(rows_out, 16) || rows_out_stride % 8 || rows_out_stride < r + d_rope)) return LKV_ERR_INVALID_ARG;
   if (rows_out == new_rows && rows_out_stride != new_row_stride) return LKV_ERR_INVALID_ARG;
