@@ -311,7 +311,8 @@ lkv_status lkv_latent_cache_append_fp8(const void* new_rows, int64_t new_row_str
  *   x          [n_tok, heads, d] bf16 or fp32 (dtype), unit inner stride, strides in elements
  *   positions  [n_tok] int32;  freqs [rot / 2] fp64, radians a position (long-context scalings change
  *              freqs and gain).  Angles are taken in fp64, products in fp32.
- *   out        as x; the same array and strides (in place) or one that does not overlap x
+ *   out        as x; the same array and strides (in place) or one that does not overlap x; no two of its
+ *              rows (of d columns) overlap
  * rot even, at most 1024, heads at most 2^20 (LKV_ERR_UNSUPPORTED); gain finite and > 0.  n_tok = 0 launches nothing.
  */
 lkv_status lkv_rope_rotate(const void* x, int64_t x_token_stride, int64_t x_head_stride,

@@ -59,6 +59,20 @@ lkv_status check_pool(Paged* g, const void* pool, int64_t page_stride, int64_t r
   return LKV_OK;
 }
 
+// Whether two of the rows of d elements at token * ts + head * hs share one.
+bool rows_overlap(int64_t ts, int64_t n_tok, int64_t hs, int64_t heads, int64_t d) {
+  ts = ts < 0 ? -ts : ts;  // a sign mirrors the rows' order
+  hs = hs < 0 ? -hs : hs;
+  if ((n_tok > 1 && ts < d) || (heads > 1 && hs < d)) return true;
+  if (n_tok == 1 || heads == 1) return false;
+  if ((hs - d) / ts >= n_tok - 1 || (ts - d) / hs >= heads - 1) return false;  // one kind of rows lies within the other's steps
+  for (int64_t h = 1; h < heads; ++h) {  // interleaved: the tokens nearest to h heads' distance
+    const int64_t t = h * hs / ts, past = h * hs - t * ts;
+    if ((past < d && t < n_tok) || (ts - past < d && t + 1 < n_tok)) return true;
+  }
+  return false;
+}
+
 template <typename T, int V>
 void launch_rope(const RopeParams& p, bool interleaved, dim3 blocks, dim3 threads, cudaStream_t s) {
   if (interleaved)
@@ -181,6 +195,7 @@ lkv_status lkv_rope_rotate(const void* x, int64_t x_token_stride, int64_t x_head
   const int size = dtype == LKV_BF16 ? 2 : 4, wide = 16 / size;
   if (!al(x, size) || !al(out, size) || !al(positions, 4) || !al(freqs, 8)) return LKV_ERR_INVALID_ARG;
   if (n_tok == 0) return LKV_OK;
+  if (rows_overlap(out_token_stride, n_tok, out_head_stride, heads, d)) return LKV_ERR_INVALID_ARG;
   RopeParams p;
   p.x = x;
   p.out = out;
