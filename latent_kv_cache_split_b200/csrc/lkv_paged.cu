@@ -1,5 +1,6 @@
 // Host side of the paged 4-bit cache (include/lkv.h): rotary positions, the append that rotates and
 // quantises, and decode attention over the pool.  Argument checks make no CUDA call.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -230,7 +231,7 @@ lkv_status lkv_rope_rotate(const void* x, int64_t x_token_stride, int64_t x_head
   } else {
     int loads = 16;
     while (loads > 1 && n_tok * ((heads + loads * by - 1) / (loads * by)) < 2048) --loads;
-    const int chunks = (heads + loads * by - 1) / (loads * by);
+    const int most = 65535, chunks = std::min((heads + loads * by - 1) / (loads * by), most);  // a grid's second dimension
     p.head_block = (heads + chunks - 1) / chunks;
   }
   const int64_t nx = (n_tok + p.tok_block - 1) / p.tok_block;
