@@ -306,25 +306,21 @@ __device__ __forceinline__ void tmem_store_rows(uint32_t taddr, const float (&v)
   }
 }
 
-// Reduce RW values (rows) of every lane over the warp's lanes: lane l ends with row l % RW.
-template <bool kMax, int RW>
-__device__ __forceinline__ float paged_rows_reduce(float (&v)[RW], int lane) {
+// Sum RW values (rows) of every lane over the warp's lanes: lane l ends with row l % RW.
+template <int RW>
+__device__ __forceinline__ float paged_rows_sum(float (&v)[RW], int lane) {
 #pragma unroll
   for (int s = RW / 2; s >= 1; s >>= 1) {
     const bool up = (lane & s) != 0;
 #pragma unroll
     for (int j = 0; j < s; ++j) {
       const float got = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + s], s);
-      const float keep = up ? v[j + s] : v[j];
-      v[j] = kMax ? fmaxf(keep, got) : keep + got;
+      v[j] = (up ? v[j + s] : v[j]) + got;
     }
   }
   float x = v[0];
 #pragma unroll
-  for (int s = RW; s < 32; s <<= 1) {
-    const float got = __shfl_xor_sync(0xffffffffu, x, s);
-    x = kMax ? fmaxf(x, got) : x + got;
-  }
+  for (int s = RW; s < 32; s <<= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
   return x;
 }
 
@@ -1094,7 +1090,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
       // the group with the last tile loads Q: that tile's QK, the unit's last, is done
       if (have_nx && grp == (NG == 2 ? n_last & 1 : 0)) load_q(nx);
       float lt[4];
-      exchange(paged_rows_reduce<false, RW>(l, lane), lt);
+      exchange(paged_rows_sum<RW>(l, lane), lt);
       const int f = seg & 1;
       if (q4 == 0 && lane < RW) {
         sm.fin_m[f][grp][rb + lane] = m_run;
