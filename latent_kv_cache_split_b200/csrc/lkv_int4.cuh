@@ -150,10 +150,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_int4_kernel(const Appen
     int begin, end, len;
     b = request_of(p.cu_new, p.pages.seq_lens, p.batch, w, lane, begin, end, len);
     if (w < begin || w >= end) return;  // behind the last request's rows
-    pos = len - (end - static_cast<int>(w));
+    pos = max(len, 0) - (end - static_cast<int>(w));
   } else {
     b = static_cast<int>(w / p.per);
-    pos = __ldg(p.pages.seq_lens + b) - p.per + static_cast<int>(w - static_cast<long long>(b) * p.per);
+    pos = max(__ldg(p.pages.seq_lens + b), 0) - p.per + static_cast<int>(w - static_cast<long long>(b) * p.per);
   }
   if (pos < 0) return;  // an idle slot: no such token
   const long long at = paged_row(p.pages, b, pos);

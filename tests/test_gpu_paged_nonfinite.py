@@ -99,3 +99,17 @@ def test_the_older_query_loses_the_columns_held_as_nan_alone(L, gpu, d, G, H, pa
     keep[0, 1, :h] = False
     keep[0, 0, :h, 32:64] = False
     assert torch.equal(out[keep], clean[keep]) and torch.isfinite(clean).all()
+
+
+def test_append_skips_the_rows_of_the_least_length(L, gpu):
+    """A length of 0 or less is an idle slot, the least int32 too: its rows have no place and no error is recorded."""
+    r, rows = 32, torch.ones((4, 32 + D_ROPE), dtype=torch.bfloat16, device=gpu)
+    pool = torch.zeros((2, 1 << 20, 160), dtype=torch.uint8, device=gpu)
+    table = torch.tensor([[0] * 4, [1] * 4], dtype=torch.int32, device=gpu)
+    for least in (-(1 << 31), -(1 << 31) + 1, -3, 0):
+        n = torch.tensor([least, 2], dtype=torch.int32, device=gpu)
+        for cu in (None, torch.tensor([0, 2, 4], dtype=torch.int32, device=gpu)):
+            L.paged_append_int4(rows, pool, r, table, n, cu_new=cu)
+            torch.cuda.synchronize()
+            assert L.check_device(clear=True) == 0
+    assert (pool[0] == 0).all() and (pool[1, :2] != 0).any() and (pool[1, 2:] == 0).all()
