@@ -583,12 +583,34 @@ def rope_frequencies(rot: int, base: float = 10000.0, factor: float = 1.0, conte
     return f.to(device), gain
 
 
+def _apart(t):
+    """Whether every dimension's steps pass over what the shorter ones span, so that no two elements share a place."""
+    span = 0
+    for stride, size in sorted(zip(t.stride(), t.shape)):
+        if size > 1:
+            if stride <= span:
+                return False
+            span += (size - 1) * stride
+    return True
+
+
+def _tokens(t, heads, d):
+    """t [..., heads, d] as [tokens, heads, d], None where its leading dimensions have no common stride."""
+    if t.dim() == 3:
+        return t
+    try:
+        return t.view(-1, heads, d)
+    except RuntimeError:
+        return None
+
+
 def rope_rotate(x, positions, freqs, first=0, interleaved=False, inverse=False, gain=1.0, out=None, stream=None):
     """Rotate columns first .. first + 2 len(freqs) - 1 of every head of x [..., heads, d] (bf16 or fp32, unit inner
     stride) to the tokens' positions (int32, one for each token of x's leading dimensions); the other columns are
     copied.  Pairs are columns (i, i + rot / 2) of that part, or (2i, 2i + 1) if interleaved.  inverse=True applies
     the transpose: the gradient of x from the gradient of the result.  out: a new tensor, or x itself (in place), or
-    one that does not overlap x.  Returns out."""
+    one that does not overlap x; none of its elements share memory.  Where leading dimensions do not flatten to one
+    stride (x[:, 1:] of [batch, tokens, heads, d]) there is a launch for each index of the first.  Returns out."""
     dtype = x.dtype
     if dtype != torch.bfloat16 and dtype != torch.float32:
         raise TypeError(f"unsupported dtype {dtype}")
@@ -605,13 +627,19 @@ def rope_rotate(x, positions, freqs, first=0, interleaved=False, inverse=False, 
     elif out.shape != shape or out.stride(-1) != 1 or (out.data_ptr() == x.data_ptr() and out.stride() != x.stride()):
         raise ValueError("out must have x's shape and unit inner stride, and x's strides if it is x's memory")
     heads, d = shape[-2:]
-    xs, os_ = (x, out) if len(shape) == 3 else (x.view(-1, heads, d), out.view(-1, heads, d))
-    n = xs.shape[0]
+    n = math.prod(shape[:-2])
     if positions.numel() != n:
         raise ValueError("positions must hold one position for each token")
     if freqs.dim() != 1 or not freqs.is_contiguous() or not positions.is_contiguous():
         raise ValueError("freqs must be [rot / 2]; freqs and positions contiguous")
     if n == 0 and heads > 0 and d > 0:
+        return out
+    xs, os_ = _tokens(x, heads, d), _tokens(out, heads, d)
+    if xs is None or os_ is None:
+        if not _apart(out):
+            raise ValueError("out has elements that share memory")
+        for one, pos, res in zip(x, positions.view(shape[:-2]), out):
+            rope_rotate(one, pos, freqs, first, interleaved, inverse, gain, res, stream)
         return out
     x_ts, x_hs, _ = xs.stride()
     o_ts, o_hs, _ = os_.stride()
