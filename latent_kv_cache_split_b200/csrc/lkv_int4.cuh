@@ -109,14 +109,15 @@ __device__ __forceinline__ int request_of(const int* cu, const int* seq_lens, in
 }
 
 // One warp a row: lane l takes columns 8 (l + 32 k) .. + 7, so 4 lanes share a scale and every load and
-// store of the warp is contiguous.  Bound by memory (2 (r + d_rope) bytes in, the row out).
+// store of the warp is contiguous.  Bound by instruction issue, some 600 a row: 78k rows of 576 take 36.4 us
+// where their bytes (the row in, the cache's row and the held values out) would take 22.5.
 //
 // The code is x / s rounded to the nearest integer, ties to even, without a division: x is 8 significant
 // bits and s = n 2^k with n in 8 .. 15, so x / s is a tie or at least 1/1920 away from one.  fma(x, 1 / s,
 // 1536) rounds x / s (off by under 2^-20) to a multiple of 2^-13, which puts ties back on the tie and
 // moves nothing else across one; adding 12582920 - 1536 then rounds to an integer, and leaves code + 8 in
 // the low bits of the sum's pattern.  A block with a NaN or an infinity gets a NaN for its scale, whatever
-// its codes (78k rows of 576: 35.8 -> 36.2 us for the maximum that keeps NaN).
+// its codes (78k rows of 576: 36.0 us with a maximum that passes over NaN, 36.4 with one that keeps it).
 __global__ void __launch_bounds__(kAppendThreads) append_int4_kernel(const AppendParams p) {
   const int lane = threadIdx.x & 31;
   const long long w = (static_cast<long long>(blockIdx.x) * kAppendThreads + threadIdx.x) >> 5;

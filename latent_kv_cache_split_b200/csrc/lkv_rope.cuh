@@ -6,8 +6,9 @@
 // the rotated part in the half layout and (2i, 2i + 1) in the interleaved one.
 //
 // The angle is taken in turns, in fp64: fp32 would lose it (at position 10^6 an fp32 angle of frequency
-// 1 is off by 0.03 rad).  p f / 2 pi is off by at most 3 ulp, under 10^-7 turns at the largest int32
-// position; its distance to the nearest whole turn is rounded to fp32 (2^-24 of it) for sincospif.
+// 1 is off by 0.03 rad).  p f / 2 pi takes three roundings (1 / 2 pi and two products), 3 2^-53 of it: below
+// 1.2 10^-7 turns at the largest int32 position and frequency 1, in proportion to the frequency.  Its distance to
+// the nearest whole turn is rounded to fp32 (2^-24 of it) for sincospif.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -59,10 +60,13 @@ struct alignas(sizeof(T) * V) RopeVec {
 
 // Threads x run along a head's items, threads y along the block's (token, head) rows.  An item is V columns of the half
 // layout's lower half with their partners, 2 columns or V of the interleaved layout, or V copied columns.  Every element
-// is read and written once, by one thread, so x and out may be the same array.  The kernel is bound by memory, and what it
-// takes is warps: one row a thread at a time with eight blocks an SM reads and writes 8192 x 128 x 192 bf16 in 152-158 us
-// (5.1-5.3 TB/s), four rows at a time with the four blocks that their registers leave in 214 us.  A block's (cos, sin) table
-// costs one fp64 angle a pair and is shared by its heads; its first loads are issued before the table is built.
+// is read and written once, by one thread, so x and out may be the same array.  With many heads the kernel is bound by memory,
+// and what it takes is warps: one row a thread at a time with eight blocks an SM reads and writes 8192 x 128 x 192 bf16,
+// interleaved, in 156 us (5.1 TB/s), four rows at a time with the four blocks that their registers leave in 214 us.  Eight
+// blocks leave 32 registers, of which the half layout in bf16 spills a few: 175 us (4.6 TB/s).  A block's (cos, sin) table
+// costs one fp64 angle a pair and is shared by its heads; its first loads are issued before the table is built.  With one
+// head there is nothing to share and the angles bound it: 65536 x 1 x 64 bf16 takes 13 us interleaved and 14 us in halves,
+// 1.2-1.3 TB/s.
 template <typename T, int V, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const __grid_constant__ RopeParams p) {
   __shared__ float2 table[kRopeTable];
