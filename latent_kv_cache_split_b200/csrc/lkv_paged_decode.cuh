@@ -183,8 +183,8 @@ struct PagedCfg {
   static constexpr int kVBoxes = D / 64;
   static constexpr int kVStage = kVBoxes * kBox;  // the state in shared memory: the value operand
   // QK takes the state from TMEM where that has the columns (an MMA with both operands in shared memory reads 4 KB of
-  // A there, 32 cycles of its bandwidth; from TMEM it runs at the tensor core's rate, 16 cycles at N = 32), else from
-  // the value operand's tile.
+  // A there, 32 cycles of its bandwidth; from TMEM it runs at the tensor core's rate, 16 cycles at N = 32; GTA 385 -> 378 us,
+  // not measured apart at d = 256), else from the value operand's tile.
   static constexpr bool kTS = D <= 256;
   // QK reads the RoPE key from the raw tile (the copy leaves it as an MMA wants it) where the ring is deep enough to hold
   // the tile that long, else the converters put it into TMEM.
@@ -690,10 +690,12 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
     }
   } else if (warp >= 4 + kPagedSoft) {
     // ================================================================== converters
-    // Warp w takes 16 keys of every tile: lanes 16 (w / 4) .. + 15 of the TMEM quadrant w % 4.  Thread 4g + 2h + b has
-    // key g + 8b and of it the 32-column chunks h + 2m (m = 0, 1 in every 128 columns) and the 16-byte pieces h + 2m of
-    // the RoPE key, which is how tcgen05.st 16x64b spreads a warp's registers; the K index of QK runs through the
-    // columns in that order, and Q is stored to match.  Where they load for themselves, the next tile's loads are issued
+    // One group (kTurns = 1): warp w takes 16 keys of every tile, lanes 16 (w / 4) .. + 15 of the TMEM quadrant w % 4.  Two
+    // groups (2): warp w takes the 32 keys of quadrant w % 4 of every second tile, from tile w / 4 on, as two times 16; a
+    // tile's barriers then count the four warps of its group.  Of 16 keys thread 4g + 2h + b has key g + 8b and of it the
+    // 32-column chunks h + 2m (m = 0, 1 in every 128 columns) and the 16-byte pieces h + 2m of the RoPE key, which is how
+    // tcgen05.st 16x64b spreads a warp's registers; the K index of QK runs through the columns in that order, and Q is
+    // stored to match.  Where they load for themselves, the next tile's loads are issued
     // when this one is converted; its rows were asked into L2 a tile earlier, and their page numbers one tile before.
     constexpr int kKeys = 16, kH = D / 128, kHalves = Cfg::kTurns;
     const int cw = warp - (4 + kPagedSoft), turn = kHalves == 2 ? cw >> 2 : 0, key0 = 32 * (cw & 3) + 16 * (kHalves == 2 ? 0 : cw >> 2);
@@ -935,7 +937,7 @@ __global__ void __launch_bounds__(kPagedThreads, 1) paged_decode_kernel(const __
       }
     }
   } else if (warp >= 4) {
-    // ================================================================== softmax / epilogue (warp 3 is idle)
+    // ================================================================== softmax / epilogue
     const int sw = warp - 4;
     const int q4 = warp & 3;                     // TMEM lane quadrant
     const int set = sw >> 2;
