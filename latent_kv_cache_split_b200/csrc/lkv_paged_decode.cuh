@@ -18,7 +18,7 @@
 // first tile's maximum, raised only when some score passes it by 8, so by 24 the maximum it was set to
 // (log2 units; a weight's relative precision does not depend on it).  Weights of a row's largest score
 // so far lie between 2^-16 and 2^8: a sum of 2^20 of them times values below 2^100, as the cache may
-// hold, stays below fp32's 2^128, and the least values, 2^-102, keep their place above 2^-126.  A tile
+// hold, stays below fp32's 2^128, and the least values, 2^-103, keep their place above 2^-126.  A tile
 // then needs no reduction over its keys, only a vote of the softmax warps on whether any score passed.
 //
 // Warps: 0 QK issuer and TMEM owner, 1 PV issuer, 2 and 3 the copies of codes, scales and RoPE keys (idle where the
